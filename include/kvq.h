@@ -10,6 +10,10 @@
  *   kivi_pack, kivi_decode_attn   packed KIVI storage and decode attention over it
  *   kivi_update, kivi_trim, kivi_packed_update, kivi_packed_trim   the KIVI cache protocol
  *   kvq_*_side             fp16 attention sinks and outlier side channel on the symmetric path
+ *   kvq_qk_norm_rope       per-head norm of queries and keys with the position rotation
+ *   kvq_prompt_attn        causal attention over whole prompts, packed sequences
+ *   kvq_tree_attn, kvq_tree_commit   attention of drafted tokens over the packed pages, and the
+ *                          move of the accepted ones into place
  * plus host helpers: packed_dim, the KIVI residual boundary, and a page allocator.
  *
  * Conventions shared by every entry point
@@ -62,6 +66,8 @@ typedef enum kvq_status {
 #define KVQ_DEVERR_PAGE_RANGE 1  /* a page id or logical page was out of range (row skipped)   */
 #define KVQ_DEVERR_TIMEOUT 2     /* a bounded wait for an asynchronous copy gave up (the
                                     affected output is invalid; the kernel returned normally)  */
+#define KVQ_DEVERR_INDEX 4       /* a length, offset, parent or node number in device memory
+                                    contradicts the call's bounds (what it concerns is skipped) */
 
 /* Maximum number of tensors one quant/dequant/KIVI call may batch, and of layers per decode
  * attention call. */
@@ -531,6 +537,155 @@ KVQ_API kvq_status kvq_decode_attn_noalloc(const kvq_pool* k_pools, const kvq_po
                                            const int32_t* seq_lens, int nseq, int max_seq_len,
                                            float softmax_scale, float* out, int32_t* dev_err,
                                            kvq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Norms of queries and keys with the position rotation
+ * ------------------------------------------------------------------------------------------ */
+
+/* Element type of the 16-bit tensors below (passed as their bit patterns). */
+typedef enum kvq_dtype { KVQ_F16 = 0, KVQ_BF16 = 1 } kvq_dtype;
+
+/*
+ * Host: the rotation frequencies inv_freq[i] (radians per position, finite, >= 0) as
+ * kvq_qk_norm_rope reads them, phases[i] = round(frac(inv_freq[i] / 2 pi) * 2^64) mod 2^64: turns
+ * per position in units of 2^-64.  A position times a phase, modulo 2^64, is the angle without
+ * any loss for far positions.  Errors: KVQ_ERR_NULL, KVQ_ERR_RANGE.
+ */
+KVQ_API kvq_status kvq_rope_phases(const double* inv_freq, int n, uint64_t* phases);
+
+/*
+ * What stands between the projections and the cache: for every token t and head, the row x (D
+ * values) becomes
+ *   y_d = x_d / sqrt(mean_d x_d^2 + eps) * w_d                  (w NULL: y = x, no norm)
+ * and then its first rotary_dim values are rotated in pairs (a, b), pair i by the angle
+ * positions[t] * inv_freq[i]:  a' = a cos - b sin,  b' = b cos + a sin, with (a, b) =
+ * (y_i, y_{i + rotary_dim / 2}), or (y_{2i}, y_{2i+1}) if interleaved.  Computed in float32 from
+ * the inputs, rounded once to the output type.
+ * q, k           device, `dtype`, [num_tokens][heads][D], a token's heads contiguous, tokens
+ *                q_stride / k_stride elements apart (a multiple of 8, >= heads * D): views into a
+ *                fused projection's output are fine.  num_tokens may be 0.
+ * q_out, k_out   the same with their own strides; q_out == q (k_out == k) with equal strides runs
+ *                in place, any other overlap is a caller error.
+ * positions      device int32 [num_tokens]; phases device uint64 [rotary_dim / 2] (may be NULL if
+ *                rotary_dim is 0).
+ * q_weight, k_weight  device float32 [D], 16-byte aligned, or NULL.
+ * head_dim a multiple of 8 in [8, 256]; rotary_dim a multiple of 16 in [0, head_dim].
+ * Errors: KVQ_ERR_SHAPE (dtype, heads < 1, head_dim, rotary_dim, strides), KVQ_ERR_NULL,
+ * KVQ_ERR_ALIGN (16 bytes; phases 8), KVQ_ERR_RANGE (num_tokens < 0, eps not finite or < 0),
+ * KVQ_ERR_CUDA.
+ */
+KVQ_API kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64_t q_stride,
+                                    const uint16_t* k, int64_t k_stride, uint16_t* q_out,
+                                    int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride,
+                                    int num_tokens, int num_q_heads, int num_kv_heads,
+                                    int head_dim, int rotary_dim, int interleaved,
+                                    const int32_t* positions, const uint64_t* phases,
+                                    const float* q_weight, const float* k_weight, float eps,
+                                    kvq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Attention over whole prompts
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * Causal attention of many query rows per sequence, the prompt's counterpart of kvq_decode_attn:
+ * sequence s has new tokens cu_q[s] .. cu_q[s+1]-1 of q and keys cu_k[s] .. cu_k[s+1]-1 of k, v,
+ * of which the last belong to the new tokens, so that new token i of Lq sees keys
+ * 0 .. i + Lk - Lq (Lk == Lq: a whole prompt; Lk > Lq: its next chunk, or with Lq == 1 one decode
+ * step, over keys held in 16 bits, e.g. by kvq_dequant_paged):
+ *   out[i][j][:] = sum_t softmax(softmax_scale * q[i][j] . k[t][h])_t v[t][h][:],  h = j / (Hq/H)
+ * with the softmax's sums in float32 and its weights rounded to the input type for the product
+ * with v.  A row that sees no key gets 0 (and lse -inf).  Values of keys and of v that a row does
+ * not see (infinities and NaN too) do not reach it.
+ * q, k, v    device, `dtype`, [total_q][Hq][D] and [total_k][H][D], a token's heads contiguous,
+ *            tokens *_stride elements apart (a multiple of 8, >= heads * D).
+ * cu_q, cu_k device int32 [nseq+1], non-decreasing, at most total_q / total_k.  Rows of out (and
+ *            lse) that belong to no sequence are left as they were.
+ * max_q, max_k  host upper bounds on a sequence's new tokens and keys.  A sequence that exceeds
+ *            them, or whose offsets are out of range, is skipped (KVQ_DEVERR_INDEX).
+ * out        `dtype` [total_q][Hq][D]; lse float32 [total_q][Hq] or NULL: the natural logarithm of
+ *            each row's sum of exponentials, by which results over different keys are joined.
+ * workspace  device scratch of at least kvq_prompt_attn_workspace(...) bytes, 16-byte aligned, no
+ *            initialisation needed; two calls that may overlap need one each.
+ * dev_err    may be NULL; also gets KVQ_DEVERR_TIMEOUT.
+ * head_dim 64, 128 or 256; any Hq that is a multiple of H, at most 128 query heads per KV head.
+ * Results do not depend on the other sequences of the call or on timing.
+ * Errors: KVQ_ERR_SHAPE (dtype, heads, head_dim, strides), KVQ_ERR_NULL, KVQ_ERR_ALIGN,
+ * KVQ_ERR_RANGE (counts; softmax_scale not finite or <= 0), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
+ */
+KVQ_API size_t kvq_prompt_attn_workspace(int nseq, int total_q, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int max_q, int max_k);
+
+KVQ_API kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_t q_stride,
+                                   const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                   int64_t v_stride, int num_q_heads, int num_kv_heads,
+                                   int head_dim, const int32_t* cu_q, const int32_t* cu_k,
+                                   int nseq, int total_q, int total_k, int max_q, int max_k,
+                                   float softmax_scale, uint16_t* out, float* lse,
+                                   void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                   kvq_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Trees of drafted tokens over the packed pages
+ * ------------------------------------------------------------------------------------------ */
+
+#define KVQ_MAX_NODES 64  /* drafted tokens per sequence */
+
+/*
+ * Attention of a tree of drafted tokens: sequence s holds seq_lens[s] tokens, and its drafts,
+ * nodes 0 .. n-1 (n = cu_nodes[s+1] - cu_nodes[s], at most max_nodes), have been appended behind
+ * them with kvq_quant_pack_paged (start_pos = seq_lens, cu_new_tokens = cu_nodes), so that node i
+ * is token seq_lens[s] + i of the pages.  parents[cu_nodes[s] + i] is the node that node i follows
+ * (in [0, i)), or -1 if it follows the cached text.  Node i sees every cached token, its ancestors
+ * and itself; otherwise the arithmetic is that of kvq_decode_attn, with the softmax weights
+ * rounded to fp16 for the product with v_hat and the result rounded to fp16.  A chain (parents
+ * i - 1) attends like n decode steps.
+ * q, out     device fp16 [n_layers][total_nodes][num_q_heads][D], 16-byte aligned.  Rows of out
+ *            that belong to no sequence are left as they were.
+ * page_table, seq_lens, max_pages, k_pools, v_pools, dev_err  as for kvq_decode_attn; cu_nodes
+ *            device int32 [nseq+1], non-decreasing, at most total_nodes; parents device int32
+ *            [total_nodes].
+ * max_nodes  host upper bound on a sequence's drafts, in [1, KVQ_MAX_NODES]; max_seq_len host
+ *            upper bound on seq_lens[s] plus its drafts.  A sequence that exceeds them is skipped
+ *            (KVQ_DEVERR_INDEX); a parent outside [-1, i) counts as -1 (KVQ_DEVERR_INDEX).  Tokens
+ *            whose page id is out of range are not attended (KVQ_DEVERR_PAGE_RANGE).
+ * workspace  kvq_tree_attn_workspace(...) bytes, 16-byte aligned, no initialisation needed; two
+ *            calls that may overlap need one each.
+ * Values of drafts that a node does not see (infinities and NaN too) do not reach it.
+ * head_dim 256; page_size a multiple of 16; at most 16 query heads per KV head.
+ * Errors: KVQ_ERR_SHAPE, KVQ_ERR_BITS, KVQ_ERR_NULL, KVQ_ERR_ALIGN, KVQ_ERR_RANGE,
+ * KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
+ */
+KVQ_API size_t kvq_tree_attn_workspace(int n_layers, int nseq, int total_nodes, int num_kv_heads,
+                                       int num_q_heads, int head_dim, int max_nodes,
+                                       int max_seq_len);
+
+KVQ_API kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_pools, int n_layers,
+                                 const uint16_t* q, int num_q_heads, const int32_t* page_table,
+                                 int max_pages, const int32_t* seq_lens, const int32_t* cu_nodes,
+                                 const int32_t* parents, int nseq, int total_nodes, int max_nodes,
+                                 int max_seq_len, float softmax_scale, uint16_t* out,
+                                 void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                 kvq_stream_t stream);
+
+/*
+ * Keep the accepted drafts: for sequence s and i = 0, 1, ..., the packed row (codes and scale, of
+ * every head, in every pool) of token seq_lens[s] + accept[cu_accept[s] + i] is copied to token
+ * seq_lens[s] + i.  All of a sequence's rows are read before any is written, so any order of node
+ * numbers, repeated ones too, is fine.  seq_lens is not advanced: the caller adds the count.
+ * pools      host array [n_tensors] (all with the same bits, num_heads, head_dim, page_size): the
+ *            K and V pools of every layer.
+ * cu_accept  device int32 [nseq+1], non-decreasing, at most total_accept; accept device int32
+ *            [total_accept], node numbers in [0, KVQ_MAX_NODES).  A sequence with more than
+ *            KVQ_MAX_NODES of them, or offsets out of range, is skipped, and a row whose node
+ *            number is out of range is (KVQ_DEVERR_INDEX); a row whose page id is out of range is
+ *            skipped too (KVQ_DEVERR_PAGE_RANGE).
+ * Errors: those of kvq_quant_pack_paged.
+ */
+KVQ_API kvq_status kvq_tree_commit(const kvq_pool* pools, int n_tensors, const int32_t* page_table,
+                                   int max_pages, const int32_t* seq_lens,
+                                   const int32_t* cu_accept, const int32_t* accept, int nseq,
+                                   int total_accept, int32_t* dev_err, kvq_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -23,6 +23,8 @@ LIB_PATH = os.path.join(_HERE, "libkvq.so")
 KVQ_MAX_TENSORS = 64
 KVQ_DEVERR_PAGE_RANGE = 1
 KVQ_DEVERR_TIMEOUT = 2
+KVQ_DEVERR_INDEX = 4
+KVQ_MAX_NODES = 64
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_BITS", 2: "KVQ_ERR_SHAPE", 3: "KVQ_ERR_NULL",
           4: "KVQ_ERR_ALIGN", 5: "KVQ_ERR_RANGE", 6: "KVQ_ERR_CUDA", 7: "KVQ_ERR_NOMEM",
           8: "KVQ_ERR_WORKSPACE"}
@@ -113,6 +115,15 @@ def _load() -> ctypes.CDLL:
         "kivi_decode_attn_workspace": (S, [I, I, I, I, I, I]),
         "kivi_decode_attn": (I, [ctypes.POINTER(kivi_packed), P, P, I, P, I, I, I, F, P, P, S,
                                  P, P]),
+        "kvq_rope_phases": (I, [P, I, P]),
+        "kvq_qk_norm_rope": (I, [I, P, I64, P, I64, P, I64, P, I64, I, I, I, I, I, I, P, P, P, P, F, P]),
+        "kvq_prompt_attn_workspace": (S, [I, I, I, I, I, I, I]),
+        "kvq_prompt_attn": (I, [I, P, I64, P, I64, P, I64, I, I, I, P, P, I, I, I, I, I, F, P, P,
+                                P, S, P, P]),
+        "kvq_tree_attn_workspace": (S, [I, I, I, I, I, I, I, I]),
+        "kvq_tree_attn": (I, [pool_p, pool_p, I, P, I, P, I, P, P, P, I, I, I, I, F, P, P, S, P,
+                              P]),
+        "kvq_tree_commit": (I, [pool_p, I, P, I, P, P, P, I, I, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -728,6 +739,200 @@ def decode_workspace(k_pools: Sequence[Pool], nseq: int, num_q_heads: int, max_s
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
+# --------------------------------------------------------------- queries, keys and whole prompts
+KVQ_F16, KVQ_BF16 = 0, 1
+_DTYPES = {torch.float16: KVQ_F16, torch.bfloat16: KVQ_BF16}
+
+
+def _here(t, name: str, dtype=None, dims: int | None = None):
+    """A contiguous tensor of the current device (the one whose stream the call uses)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dims is not None and t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    return t
+
+
+def _head_rows(t, name: str, like=None) -> int:
+    """Checks [tokens, heads, D] rows of 16-bit values, a token's heads contiguous, and returns the
+    elements between tokens."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES or (like is not None and t.dtype != like.dtype):
+        raise TypeError(f"{name} must be float16 or bfloat16, all alike, got {t.dtype}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if n > 1 else -(-h * d // 8) * 8
+
+
+def _opt(t, name: str, dtype, dims: int | None = None):
+    return None if t is None else _here(t, name, dtype, dims).data_ptr()
+
+
+def _workspace(t) -> tuple[int, int]:
+    _here(t, "workspace")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def kvq_rope_phases(inv_freq, device="cuda") -> torch.Tensor:
+    """The rotation frequencies (radians per position, [rotary_dim / 2]) as kvq_qk_norm_rope reads
+    them: an int64 tensor on `device`, made once per model."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64).reshape(-1).cpu().contiguous()
+    out = torch.empty(f.numel(), dtype=torch.int64)
+    _check(_lib.kvq_rope_phases(f.data_ptr(), f.numel(), out.data_ptr()))
+    return out.to(device)
+
+
+def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_out: torch.Tensor, k_out: torch.Tensor,
+                     positions: torch.Tensor, phases: torch.Tensor | None = None,
+                     q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                     eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """Norm (where a weight is given) and position rotation (over 2 * phases.numel() channels) of
+    every row of q [tokens, Hq, D] and k [tokens, H, D] into q_out, k_out (q and k themselves to
+    work in place).  fp16 or bf16; tokens may be strided (views of a fused projection)."""
+    qs, ks = _head_rows(q, "q"), _head_rows(k, "k", q)
+    qos, kos = _head_rows(q_out, "q_out", q), _head_rows(k_out, "k_out", q)
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out / k_out must have q's / k's shape")
+    n, hq, d = q.shape
+    if k.shape[0] != n or k.shape[2] != d:
+        raise ValueError("q and k must have the same tokens and head_dim")
+    _here(positions, "positions", torch.int32, 1)
+    if positions.shape[0] != n:
+        raise ValueError("one position per token")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.numel() != d:
+            raise ValueError(f"{name} must have head_dim entries")
+    _check(_lib.kvq_qk_norm_rope(_DTYPES[q.dtype], q.data_ptr(), qs, k.data_ptr(), ks,
+                                 q_out.data_ptr(), qos, k_out.data_ptr(), kos, n, hq, k.shape[1],
+                                 d, 0 if phases is None else 2 * phases.numel(),
+                                 1 if interleaved else 0, positions.data_ptr(),
+                                 _opt(phases, "phases", torch.int64, 1),
+                                 _opt(q_weight, "q_weight", torch.float32),
+                                 _opt(k_weight, "k_weight", torch.float32), eps, _stream(stream)))
+
+
+def kvq_prompt_attn_workspace(nseq: int, total_q: int, num_q_heads: int, num_kv_heads: int,
+                              head_dim: int, max_q: int, max_k: int) -> int:
+    return _lib.kvq_prompt_attn_workspace(nseq, total_q, num_q_heads, num_kv_heads, head_dim,
+                                          max_q, max_k)
+
+
+def prompt_workspace(nseq: int, total_q: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                     max_q: int, max_k: int, device="cuda") -> torch.Tensor:
+    """A workspace tensor of the size kvq_prompt_attn needs."""
+    n = kvq_prompt_attn_workspace(nseq, total_q, num_q_heads, num_kv_heads, head_dim, max_q, max_k)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def kvq_prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                    cu_k: torch.Tensor, max_q: int, max_k: int, softmax_scale: float,
+                    out: torch.Tensor, workspace: torch.Tensor, lse: torch.Tensor | None = None,
+                    dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Causal attention of packed sequences: q [total_q, Hq, D] over k, v [total_k, H, D] (fp16 or
+    bf16, tokens may be strided) into out [total_q, Hq, D] (contiguous), row statistics into lse
+    float32 [total_q, Hq]."""
+    qs, ks, vs = _head_rows(q, "q"), _head_rows(k, "k", q), _head_rows(v, "v", q)
+    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+        raise ValueError("k and v must have one shape, and q's head_dim")
+    _here(out, "out", q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _here(cu_q, "cu_q", torch.int32, 1)
+    _here(cu_k, "cu_k", torch.int32, 1)
+    if cu_q.shape[0] < 1 or cu_k.shape != cu_q.shape:
+        raise ValueError("cu_q and cu_k must have nseq + 1 entries each")
+    n, hq, d = q.shape
+    if lse is not None and lse.shape != (n, hq):
+        raise ValueError("lse must be [total_q, Hq]")
+    ws, ws_bytes = _workspace(workspace)
+    _check(_lib.kvq_prompt_attn(_DTYPES[q.dtype], q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(),
+                                vs, hq, k.shape[1], d, cu_q.data_ptr(), cu_k.data_ptr(),
+                                cu_q.shape[0] - 1, n, k.shape[0], max_q, max_k, softmax_scale,
+                                out.data_ptr(), _opt(lse, "lse", torch.float32), ws, ws_bytes,
+                                _opt(dev_err, "dev_err", torch.int32), _stream(stream)))
+
+
+# --------------------------------------------------------------------- trees of drafted tokens
+def kvq_tree_attn_workspace(n_layers: int, nseq: int, total_nodes: int, num_kv_heads: int,
+                            num_q_heads: int, head_dim: int, max_nodes: int,
+                            max_seq_len: int) -> int:
+    return _lib.kvq_tree_attn_workspace(n_layers, nseq, total_nodes, num_kv_heads, num_q_heads,
+                                        head_dim, max_nodes, max_seq_len)
+
+
+def tree_workspace(k_pools: Sequence[Pool], nseq: int, total_nodes: int, num_q_heads: int,
+                   max_nodes: int, max_seq_len: int, device="cuda") -> torch.Tensor:
+    """A workspace tensor of the size kvq_tree_attn needs."""
+    p = k_pools[0]
+    n = kvq_tree_attn_workspace(len(k_pools), nseq, total_nodes, p.num_heads, num_q_heads,
+                                p.head_dim, max_nodes, max_seq_len)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _tree_table(page_table, seq_lens, cu) -> int:
+    """Checks the tensors that describe the sequences of a tree call; returns their count."""
+    _here(page_table, "page_table", torch.int32, 2)
+    _here(seq_lens, "seq_lens", torch.int32, 1)
+    nseq = seq_lens.shape[0]
+    if page_table.shape[0] < nseq or cu.dim() != 1 or cu.shape[0] != nseq + 1:
+        raise ValueError("page_table needs a row per sequence and the offsets nseq + 1 entries")
+    return nseq
+
+
+def kvq_tree_attn(k_pools: Sequence[Pool], v_pools: Sequence[Pool], q: torch.Tensor,
+                  page_table: torch.Tensor, seq_lens: torch.Tensor, cu_nodes: torch.Tensor,
+                  parents: torch.Tensor, max_nodes: int, max_seq_len: int, softmax_scale: float,
+                  out: torch.Tensor, workspace: torch.Tensor,
+                  dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of the drafts appended behind seq_lens[s] cached tokens, each over the cached
+    text, its ancestors (parents) and itself: q fp16 [n_layers, total_nodes, Hq, 256] -> out fp16.
+    max_seq_len bounds seq_lens plus the drafts."""
+    if len(k_pools) != len(v_pools):
+        raise ValueError("one V pool per K pool")
+    _here(q, "q", torch.float16, 4)
+    _here(out, "out", torch.float16)
+    _here(cu_nodes, "cu_nodes", torch.int32)
+    _here(parents, "parents", torch.int32, 1)
+    nseq = _tree_table(page_table, seq_lens, cu_nodes)
+    n_layers, total, hq, d = q.shape
+    if n_layers != len(k_pools) or out.shape != q.shape or parents.shape[0] != total:
+        raise ValueError("q and out are [n_layers, total_nodes, Hq, D], with a parent per node")
+    if d != k_pools[0].head_dim:
+        raise ValueError("q and the pools must have one head_dim")
+    ws, ws_bytes = _workspace(workspace)
+    _check(_lib.kvq_tree_attn(_pool_array(k_pools), _pool_array(v_pools), n_layers, q.data_ptr(),
+                              hq, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
+                              cu_nodes.data_ptr(), parents.data_ptr(), nseq, total, max_nodes,
+                              max_seq_len, softmax_scale, out.data_ptr(), ws, ws_bytes,
+                              _opt(dev_err, "dev_err", torch.int32), _stream(stream)))
+
+
+def kvq_tree_commit(pools: Sequence[Pool], page_table: torch.Tensor, seq_lens: torch.Tensor,
+                    cu_accept: torch.Tensor, accept: torch.Tensor,
+                    dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Move the accepted drafts (node numbers accept[cu_accept[s]:cu_accept[s + 1]]) to the places
+    behind seq_lens[s], in every pool.  seq_lens is not advanced."""
+    _here(cu_accept, "cu_accept", torch.int32)
+    _here(accept, "accept", torch.int32, 1)
+    nseq = _tree_table(page_table, seq_lens, cu_accept)
+    _check(_lib.kvq_tree_commit(_pool_array(pools), len(pools), page_table.data_ptr(),
+                                page_table.shape[1], seq_lens.data_ptr(), cu_accept.data_ptr(),
+                                accept.data_ptr(), nseq, accept.shape[0],
+                                _opt(dev_err, "dev_err", torch.int32), _stream(stream)))
+
+
 __all__ = ["KVQError", "Pool", "Allocator", "parse_mode", "kvq_version", "kvq_packed_dim",
            "kivi_boundary", "kvq_quant_pack_paged", "kvq_dequant_paged", "kivi_quant_dequant",
            "kvq_decode_attn_workspace", "kvq_decode_attn", "kvq_decode_attn_noalloc",
@@ -736,4 +941,7 @@ __all__ = ["KVQError", "Pool", "Allocator", "parse_mode", "kvq_version", "kvq_pa
            "KiviPacked", "kivi_pack", "kivi_decode_attn_workspace", "kivi_decode_attn",
            "kivi_state", "kivi_state_new", "kivi_update", "kivi_trim", "kivi_packed_update",
            "kivi_packed_trim", "kivi_unpack",
+           "kvq_rope_phases", "kvq_qk_norm_rope", "kvq_prompt_attn_workspace", "prompt_workspace",
+           "kvq_prompt_attn", "kvq_tree_attn_workspace", "tree_workspace", "kvq_tree_attn",
+           "kvq_tree_commit",
            "decode_workspace", "LIB_PATH"]
