@@ -608,8 +608,9 @@ KVQ_API kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64_t 
  * workspace  device scratch of at least kvq_prompt_attn_workspace(...) bytes, 16-byte aligned, no
  *            initialisation needed; two calls that may overlap need one each.
  * dev_err    may be NULL; also gets KVQ_DEVERR_TIMEOUT.
+ * All pointers are device memory (not a host view: tiles are read by the tensor copy engine).
  * head_dim 64, 128 or 256; any Hq that is a multiple of H, at most 128 query heads per KV head.
- * Results do not depend on the other sequences of the call or on timing.
+ * Two calls with the same arguments give the same bits.
  * Errors: KVQ_ERR_SHAPE (dtype, heads, head_dim, strides), KVQ_ERR_NULL, KVQ_ERR_ALIGN,
  * KVQ_ERR_RANGE (counts; softmax_scale not finite or <= 0), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
  */

@@ -30,6 +30,8 @@ It is a plain, slow, obviously correct numpy restatement of what the pages compu
   each row's largest-magnitude elements kept as (fp16 value, position) pairs.
   Source: VeloxQuant-MLX API docs, "veloxquant_mlx.cache.kvquant_cache module" (byte
   accounting: the fp16 outlier side channel; Attention Sink-Aware quantization).
+* ``prompt``     -- attention of many rows per sequence (whole prompts, drafted trees) and the
+  query/key norm with the position rotation, from their definitions in float64.
 * ``storage``    -- the storage arithmetic (bytes per token per KV head, whole-cache GiB).
   Source: MTPLX pull request #267, description, storage paragraph.
 
@@ -37,4 +39,4 @@ Readings taken where the pages are silent are listed in each module's docstring.
 Pins (checks against values and properties the pages and mathematics fix) live in
 ``tests/test_oracle_*.py`` and ``tests/golden/``.
 """
-from . import symmetric, kivi, kivi_packed, attention, storage, side  # noqa: F401
+from . import symmetric, kivi, kivi_packed, attention, prompt, storage, side  # noqa: F401
