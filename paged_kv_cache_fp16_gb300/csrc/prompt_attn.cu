@@ -1,96 +1,666 @@
-// Causal attention over whole prompts: one warp per (token, query head), online softmax.
+// Causal attention over whole prompts on the fifth-generation tensor cores.
+//
+// For a tile of 128 query rows and tiles of NB keys:
+//   S = Q K^T            tcgen05.mma, both operands in shared memory, S (float32) in TMEM
+//   p = 2^(S c - m)      one thread per row (c = softmax_scale log2 e), running maximum and sum
+//   O += P V             tcgen05.mma, P (16 bits) from TMEM over the place of S, O in TMEM
+// so the scores never leave the SM and a key is read once per tile of rows.
+//
+// Rows: a tile packs the G = Hq / H query heads of a KV head beside as many tokens as fit
+// (128 / G tokens x G heads), so that a short prompt or a single token still shares each key among
+// its heads.
+// Roles of the 6 warps: 4 softmax warps (thread = row = TMEM lane), one that issues the products,
+// one that issues the tensor copies.  K and V go through one ring of equal slots: a K tile as
+// pieces along the channels, a V tile as pieces along its keys, each of which is handed back when
+// its products are done.
+//
+// Per head dimension (measured on one GB300, figures beside the launch table below): at 256, O and
+// two score buffers fill TMEM, one CTA per SM, and the softmax of one tile runs under the products
+// of the next; at 128 and 64 two CTAs share an SM and cover each other's softmax.
+//
+// Keys that a row does not see: scores are set to -inf whatever they hold; in the tiles where some
+// row's view ends, V rows that no row sees are zeroed and non-finite V values that only some rows
+// see are zeroed too, and added to those rows' results at the end (0 * inf would reach the others).
+//
+// Few rows over many keys: the keys are split over CTAs, each leaves (m, l, O) and a second kernel
+// joins them.
 #include <cmath>
 #include <cstdint>
+#include <mutex>
+#include <type_traits>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "kvq_tc5.cuh"
 
 namespace kvq {
 namespace {
 
+#define kNegInf (-__int_as_float(0x7f800000))
+
+constexpr int kRows = 128;
+constexpr int kSoftmaxThreads = 128;
+constexpr int kThreads = 192;
+
+// NB: keys per tile.  KD: channels of a K slot (NB rows).  VR: keys of a V slot (D channels).
+// NS: score buffers.  kSlots: ring slots.  kCtas: resident CTAs per SM.
+template <int D> struct Cfg;
+template <> struct Cfg<256> { static constexpr int NB = 128, KD = 128, VR = 64, NS = 2, kSlots = 5, kCtas = 1; };
+template <> struct Cfg<128> { static constexpr int NB = 128, KD = 64, VR = 64, NS = 1, kSlots = 5, kCtas = 2; };
+template <> struct Cfg<64> { static constexpr int NB = 64, KD = 64, VR = 64, NS = 2, kSlots = 8, kCtas = 2; };
+
+template <int D>
+struct Lay {
+  using C = Cfg<D>;
+  static constexpr int kQ = kRows * D * 2;
+  static constexpr int kSlot = C::NB * C::KD * 2;
+  static_assert(kSlot == C::VR * D * 2, "K and V slots are alike");
+  static constexpr int kRing = kQ;
+  static constexpr int kBars = kRing + C::kSlots * kSlot;
+  static constexpr int kNumBars = 2 * C::kSlots + 3 + 2 * C::NS;
+  static constexpr int kTotal = kBars + kNumBars * 8 + 16;
+  static constexpr int kCols = C::kCtas == 1 ? 512 : 256;
+  static_assert(D + C::NS * C::NB <= kCols, "TMEM");
+  static constexpr int nk = D / C::KD, nv = C::NB / C::VR;
+};
+
 struct PromptArgs {
-  const uint16_t* q;
-  const uint16_t* k;
   const uint16_t* v;
-  int64_t qs, ks, vs;
+  int64_t vs;
   const int32_t* cu_q;
   const int32_t* cu_k;
   uint16_t* out;
   float* lse;
+  float* ws;
   int32_t* err;
-  int nseq, total_q, total_k, max_q, max_k, Hq, H;
-  float scale;
+  int nseq, total_q, total_k, max_q, max_k, Hq, H, G;
+  int tpt;        // tokens per row tile
+  int n_splits;   // CTAs along the keys
+  int tps;        // key tiles per split
+  float c;        // softmax_scale * log2(e)
 };
 
+// One row tile of one KV head of one sequence.
+struct Unit {
+  int q0, lq, k0, lk, h, tile;
+  bool found;
+};
+
+// The unit of linear index u, found by a whole warp: sequences in order, within one the KV heads,
+// within a head the tiles from the last (the most keys) to the first.  Sequences that contradict
+// the call's bounds have none; with `check` set all of them are looked at and reported.
+__device__ __forceinline__ Unit find_unit(const PromptArgs& a, int u, bool check) {
+  const int lane = threadIdx.x & 31;
+  Unit r;
+  r.found = false;
+  int64_t before = 0;
+  for (int base = 0; base < a.nseq; base += 32) {
+    const int s = base + lane;
+    int q0 = 0, q1 = 0, k0 = 0, k1 = 0, tiles = 0;
+    if (s < a.nseq) {
+      q0 = __ldg(a.cu_q + s);
+      q1 = __ldg(a.cu_q + s + 1);
+      k0 = __ldg(a.cu_k + s);
+      k1 = __ldg(a.cu_k + s + 1);
+      const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 &&
+                      k1 <= a.total_k && q1 - q0 <= a.max_q && k1 - k0 <= a.max_k;
+      if (ok) tiles = (q1 - q0 + a.tpt - 1) / a.tpt;
+      else if (check) report(a.err, KVQ_DEVERR_INDEX);
+    }
+    const int64_t mine = static_cast<int64_t>(tiles) * a.H;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(kFullMask, incl, o);
+      if (lane >= o) incl += x;
+    }
+    const int64_t start = before + incl - mine;
+    const unsigned hit = __ballot_sync(kFullMask, u >= start && u < start + mine);
+    if (hit && !r.found) {
+      const int src = __ffs(hit) - 1;
+      const int rem = __shfl_sync(kFullMask, static_cast<int>(u - start), src);
+      const int t = __shfl_sync(kFullMask, tiles, src);
+      r.q0 = __shfl_sync(kFullMask, q0, src);
+      r.lq = __shfl_sync(kFullMask, q1, src) - r.q0;
+      r.k0 = __shfl_sync(kFullMask, k0, src);
+      r.lk = __shfl_sync(kFullMask, k1, src) - r.k0;
+      r.h = rem / t;
+      r.tile = t - 1 - (rem - r.h * t);
+      r.found = true;
+      if (!check) return r;
+    }
+    before += __shfl_sync(kFullMask, incl, 31);
+  }
+  return r;
+}
+
+// Keys that token i of the sequence sees.
+__device__ __forceinline__ int keys_seen(const Unit& n, int i) {
+  return max(0, min(n.lk, i + n.lk - n.lq + 1));
+}
+
+template <bool BF> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (BF) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  } else {
+    return pack_h2(lo, hi);
+  }
+}
 template <bool BF> __device__ __forceinline__ float to_f(uint16_t b) {
   if constexpr (BF) return __uint_as_float(static_cast<uint32_t>(b) << 16);
   else return h2f(b);
 }
-template <bool BF> __device__ __forceinline__ uint16_t from_f(float f) {
-  if constexpr (BF) return __bfloat16_as_ushort(__float2bfloat16_rn(f));
-  else return f2h(f);
+// Whether either 16-bit half of w is an infinity or NaN.
+template <bool BF> __device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  constexpr uint32_t e = BF ? 0x7f80u : 0x7c00u;
+  return (w & e) == e || (w & (e << 16)) == (e << 16);
+}
+template <bool BF> __device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  constexpr uint32_t e = BF ? 0x7f80u : 0x7c00u;
+  if ((w & e) == e) w &= 0xffff0000u;
+  if ((w & (e << 16)) == (e << 16)) w &= 0x0000ffffu;
+  return w;
+}
+
+// A whole warp's bounded wait: every lane goes the same way on.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
+                                          const volatile int* gave_up) {
+  return __all_sync(kFullMask, tc5::wait(bar, parity, gave_up));
+}
+
+// A V slot before its product, in a tile where some row's view ends: key t0 + i of row i of the
+// slot.  Keys no row sees are zeroed; non-finite values that only some rows see are zeroed and
+// noted in *flag.
+template <bool BF, int D, int VR>
+__device__ __forceinline__ void clean_v(unsigned char* slot, int t0, int lim_min, int lim_max,
+                                        int* flag) {
+  bool found = false;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < VR * D / 8; i += kSoftmaxThreads) {
+    const int t = t0 + ((i >> 3) % VR);
+    if (t < lim_min) continue;
+    uint4* p = reinterpret_cast<uint4*>(slot + i * 16);
+    if (t >= lim_max) {
+      *p = make_uint4(0, 0, 0, 0);
+    } else {
+      uint4 w = *p;
+      if (nonfinite2<BF>(w.x) || nonfinite2<BF>(w.y) || nonfinite2<BF>(w.z) ||
+          nonfinite2<BF>(w.w)) {
+        w.x = finite2<BF>(w.x);
+        w.y = finite2<BF>(w.y);
+        w.z = finite2<BF>(w.z);
+        w.w = finite2<BF>(w.w);
+        *p = w;
+        found = true;
+      }
+    }
+  }
+  if (found) *flag = 1;
 }
 
 template <bool BF, int D>
-__global__ void __launch_bounds__(256) prompt_rows_kernel(const PromptArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t n_rows = static_cast<int64_t>(a.total_q) * a.Hq;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < n_rows;
-       row += step) {
-    const int t = static_cast<int>(row / a.Hq), j = static_cast<int>(row % a.Hq);
-    const int s = find_seq_from(a.cu_q, a.nseq, t, 0);
-    const int q0 = a.cu_q[s], q1 = a.cu_q[s + 1], k0 = a.cu_k[s], k1 = a.cu_k[s + 1];
-    if (t < q0 || t >= q1) continue;
-    if (q0 < 0 || q1 > a.total_q || k0 < 0 || k1 < k0 || k1 > a.total_k || q1 - q0 > a.max_q ||
-        k1 - k0 > a.max_k) {
-      report(a.err, KVQ_DEVERR_INDEX);
-      continue;
-    }
-    const int end = t - q0 + (k1 - k0) - (q1 - q0) + 1;   // keys seen
-    const int h = j / (a.Hq / a.H);
-    float qf[E], o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      qf[e] = to_f<BF>(a.q[t * a.qs + static_cast<int64_t>(j) * D + lane * E + e]);
-      o[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < end; ++i) {
-      const uint16_t* kr = a.k + (k0 + i) * a.ks + static_cast<int64_t>(h) * D + lane * E;
-      const uint16_t* vr = a.v + (k0 + i) * a.vs + static_cast<int64_t>(h) * D + lane * E;
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) x = fmaf(qf[e], to_f<BF>(kr[e]), x);
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(kFullMask, x, w);
-      x *= a.scale;
-      const float mn = fmaxf(m, x);
-      const float f = m == -INFINITY ? 0.f : expf(m - mn), p = expf(x - mn);
-      l = l * f + p;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + p * to_f<BF>(vr[e]);
-      m = mn;
-    }
-    const float inv = end > 0 ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      a.out[(static_cast<int64_t>(t) * a.Hq + j) * D + lane * E + e] = from_f<BF>(o[e] * inv);
-    if (a.lse && lane == 0)
-      a.lse[static_cast<int64_t>(t) * a.Hq + j] = end > 0 ? m + logf(l) : -INFINITY;
+__global__ void __launch_bounds__(kThreads, Cfg<D>::kCtas)
+prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap mq,
+                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using C = Cfg<D>;
+  using L = Lay<D>;
+  constexpr int NB = C::NB, NS = C::NS, SL = C::kSlots;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
+  uint64_t *full = bars, *empty = bars + SL, *qfull = bars + 2 * SL, *odone = qfull + 1,
+           *sfull = odone + 2, *pready = sfull + NS;
+  uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
+  volatile int* flags = reinterpret_cast<volatile int*>(tmem_ptr + 1);   // [0] gave up, [1] V
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Unit n = find_unit(a, blockIdx.x, blockIdx.x == 0 && blockIdx.y == 0 && warp == 0);
+  if (!n.found) return;
+  const int i0 = n.tile * a.tpt, i1 = min(i0 + a.tpt, n.lq);      // the tile's tokens
+  const int lim_min = keys_seen(n, i0), lim_max = keys_seen(n, i1 - 1);
+  const int all = (lim_max + NB - 1) / NB;                         // key tiles any row sees
+  const int j0 = blockIdx.y * a.tps, j1 = min(j0 + a.tps, all);
+  const int nt = j1 - j0;
+  if (nt <= 0 && !(all == 0 && j0 == 0)) return;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < SL; ++i) { mbar_init(full + i, 1); mbar_init(empty + i, 1); }
+    mbar_init(qfull, 1);
+    mbar_init(odone, 1);
+    mbar_init(odone + 1, 1);
+    for (int i = 0; i < NS; ++i) { mbar_init(sfull + i, 1); mbar_init(pready + i, kSoftmaxThreads); }
+    tc5::fence_barrier_init();
+    flags[0] = 0;
+    flags[1] = 0;
   }
+  if (warp == 4) tc5::tmem_alloc(tmem_ptr, L::kCols);
+  tc5::fence_before();
+  __syncthreads();
+  tc5::fence_after();
+  const uint32_t tmem = *tmem_ptr;
+
+  if (warp == 5) {
+    // ---------------------------------------------------------------- tensor copies (one thread)
+    if (lane == 0 && nt > 0) {
+      mbar_expect_tx(qfull, (D / 64) * 128 * a.tpt * a.G);
+      for (int p = 0; p < D / 64; ++p)
+        tc5::tma_load_3d(sm + p * kRows * 128, &mq, p * 64, n.h * a.G, n.q0 + i0, qfull);
+      int pos = 0;
+      bool ok = true;
+      auto slot_ready = [&]() {
+        if (pos >= SL && !tc5::wait(empty + pos % SL, (pos / SL + 1) & 1, flags)) {
+          flags[0] = 1;
+          ok = false;
+        }
+        return ok;
+      };
+      auto load_k = [&](int j) {
+        for (int i = 0; i < L::nk; ++i) {
+          if (!slot_ready()) return;
+          unsigned char* dst = sm + L::kRing + (pos % SL) * L::kSlot;
+          mbar_expect_tx(full + pos % SL, L::kSlot);
+#pragma unroll
+          for (int p = 0; p < C::KD / 64; ++p)
+            tc5::tma_load_3d(dst + p * NB * 128, &mk, i * C::KD + p * 64, n.h, n.k0 + (j0 + j) * NB,
+                             full + pos % SL);
+          ++pos;
+        }
+      };
+      auto load_v = [&](int j) {
+        for (int i = 0; i < L::nv; ++i) {
+          if (!slot_ready()) return;
+          unsigned char* dst = sm + L::kRing + (pos % SL) * L::kSlot;
+          mbar_expect_tx(full + pos % SL, L::kSlot);
+#pragma unroll
+          for (int p = 0; p < D / 64; ++p)
+            tc5::tma_load_3d(dst + p * C::VR * 128, &mv, p * 64, n.h,
+                             n.k0 + (j0 + j) * NB + i * C::VR, full + pos % SL);
+          ++pos;
+        }
+      };
+      load_k(0);
+      for (int j = 0; j < nt && ok; ++j) {
+        if constexpr (NS == 2) {
+          if (j + 1 < nt) load_k(j + 1);
+          if (ok) load_v(j);
+        } else {
+          load_v(j);
+          if (ok && j + 1 < nt) load_k(j + 1);
+        }
+      }
+      if (!ok) {   // wait for the copies in flight
+        for (int i = max(0, pos - SL); i < pos; ++i)
+          mbar_wait_bounded(full + i % SL, (i / SL) & 1);
+        mbar_wait_bounded(qfull, 0);
+      }
+    }
+  } else if (warp == 4) {
+    // ------------------------------------------------------------------- products (one thread)
+    if (lane == 0 && nt > 0) {
+      const uint32_t base = smem_u32(sm), ring = base + L::kRing;
+      const uint64_t dk = tc5::desc_base(16), dv = tc5::desc_base(C::VR * 128);
+      constexpr uint32_t id_s = tc5::idesc(BF, NB, false), id_o = tc5::idesc(BF, D, true);
+      int pos = 0;
+      bool ok = tc5::wait(qfull, 0, flags);
+      auto product_s = [&](int j) {
+        const uint32_t d = tmem + D + (j % NS) * NB;
+        for (int i = 0; i < L::nk; ++i, ++pos) {
+          ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);
+          if (!ok) return;
+          const uint32_t kb = ring + (pos % SL) * L::kSlot;
+#pragma unroll
+          for (int k = 0; k < C::KD / 16; ++k) {
+            const int kq = i * (C::KD / 16) + k;   // the contraction step within the row
+            tc5::mma_ss(d, tc5::desc_at(dk, base + (kq / 4) * kRows * 128 + (kq % 4) * 32),
+                        tc5::desc_at(dk, kb + (k / 4) * NB * 128 + (k % 4) * 32), id_s, kq > 0);
+          }
+          tc5::commit(empty + pos % SL);
+        }
+        tc5::commit(sfull + j % NS);
+      };
+      auto product_o = [&](int j) {
+        ok = ok && tc5::wait(pready + j % NS, (j / NS) & 1, flags);
+        if (!ok) return;
+        tc5::fence_after();
+        const uint32_t pb = tmem + D + (j % NS) * NB;
+        for (int i = 0; i < L::nv; ++i, ++pos) {
+          ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);
+          if (!ok) return;
+          const uint32_t vb = ring + (pos % SL) * L::kSlot;
+#pragma unroll
+          for (int k = 0; k < C::VR / 16; ++k)
+            tc5::mma_ts(tmem, pb + (i * (C::VR / 16) + k) * 8, tc5::desc_at(dv, vb + k * 2048), id_o,
+                        j > 0 || i > 0 || k > 0);
+          tc5::commit(empty + pos % SL);
+        }
+        tc5::commit(odone + (j & 1));   // two, so that no wait is a whole turn of parity behind
+      };
+      if (ok) product_s(0);
+      for (int j = 0; j < nt && ok; ++j) {
+        if constexpr (NS == 2) {
+          // the next scores go over the weights of tile j - 1, whose product was issued before:
+          // products of one CTA run in the order of their issue
+          if (j + 1 < nt) product_s(j + 1);
+          if (ok) product_o(j);
+        } else {
+          product_o(j);
+          if (ok && j + 1 < nt) product_s(j + 1);
+        }
+      }
+      if (!ok) {   // what was issued must end before the memory is given back
+        flags[0] = 1;
+        tc5::commit(qfull);
+        mbar_wait_bounded(qfull, 1);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax: thread = row
+    const int r = threadIdx.x, ri = r / a.G;
+    const int tok = i0 + ri;
+    const bool live = ri < a.tpt && tok < i1;
+    const int limit = live ? keys_seen(n, tok) : 0;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
+    float m = kNegInf, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nt; ++j) {
+      ok = warp_wait(sfull + j % NS, (j / NS) & 1, flags);
+      if (!ok) break;
+      tc5::fence_after();
+      const uint32_t sb = lanes + D + (j % NS) * NB;
+      const int t0 = (j0 + j) * NB;
+      const bool edge = t0 + NB > lim_min;
+      uint32_t s[NB];
+#pragma unroll
+      for (int q = 0; q < NB / 32; ++q) tc5::ld32(sb + q * 32, s + q * 32);
+      tc5::wait_ld32(s);
+#pragma unroll
+      for (int q = 1; q < NB / 32; ++q) tc5::after_ld32(s + q * 32);
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          if (t0 + i >= limit) s[i] = 0xff800000u;
+      }
+      float mx0 = kNegInf, mx1 = kNegInf, mx2 = kNegInf, mx3 = kNegInf;
+#pragma unroll
+      for (int i = 0; i < NB; i += 4) {
+        mx0 = fmaxf(mx0, __uint_as_float(s[i]));
+        mx1 = fmaxf(mx1, __uint_as_float(s[i + 1]));
+        mx2 = fmaxf(mx2, __uint_as_float(s[i + 2]));
+        mx3 = fmaxf(mx3, __uint_as_float(s[i + 3]));
+      }
+      const float x = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.c;
+      if (j == 0) {
+        m = x;
+      } else {
+        const bool up = x > m + tc5::kSlack;
+        if (__any_sync(kFullMask, up)) {
+          const float f = up ? ex2_fast(m - x) : 1.f;
+          if (up) m = x;
+          l *= f;
+          ok = warp_wait(odone + ((j - 1) & 1), (j - 1) >> 1 & 1, flags);
+          if (!ok) break;
+          tc5::fence_after();
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tc5::ld32(lanes + q * 32, o);
+            tc5::wait_ld32(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tc5::st32(lanes + q * 32, o);
+          }
+          tc5::wait_st();
+        }
+      }
+      const float mo = m == kNegInf ? 0.f : m - tc5::kOff;
+      float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+      for (int q = 0; q < NB / 32; ++q) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float p0 = ex2_fast(fmaf(__uint_as_float(s[q * 32 + i]), a.c, -mo));
+          const float p1 = ex2_fast(fmaf(__uint_as_float(s[q * 32 + i + 1]), a.c, -mo));
+          const float p2 = ex2_fast(fmaf(__uint_as_float(s[q * 32 + i + 2]), a.c, -mo));
+          const float p3 = ex2_fast(fmaf(__uint_as_float(s[q * 32 + i + 3]), a.c, -mo));
+          l0 += p0; l1 += p1; l2 += p2; l3 += p3;
+          p[i / 2] = pack2<BF>(p0, p1);
+          p[i / 2 + 1] = pack2<BF>(p2, p3);
+        }
+        tc5::st16(sb + q * 16, p);
+      }
+      l += (l0 + l1) + (l2 + l3);
+      tc5::wait_st();
+      if (edge) {
+        // a slot's phase is told by its parity: the load before the one waited for must be known
+        // to be over, and it is once the product of the tile before is
+        if (j > 0) ok = warp_wait(odone + ((j - 1) & 1), (j - 1) >> 1 & 1, flags);
+        const int at = (NS == 2 ? min(j + 2, nt) : j + 1) * L::nk + j * L::nv;
+        for (int i = 0; i < L::nv; ++i) {
+          const int pos = at + i;
+          ok = ok && warp_wait(full + pos % SL, (pos / SL) & 1, flags);
+          if (ok)
+            clean_v<BF, D, C::VR>(sm + L::kRing + (pos % SL) * L::kSlot, t0 + i * C::VR, lim_min,
+                                  lim_max, const_cast<int*>(flags) + 1);
+        }
+        if (!ok) break;
+        tc5::fence_smem();
+      }
+      tc5::fence_before();
+      mbar_arrive(pready + j % NS);
+    }
+    if (ok && nt > 0) ok = warp_wait(odone + ((nt - 1) & 1), (nt - 1) >> 1 & 1, flags);
+    if (!ok) flags[0] = 1;
+    tc5::fence_after();
+    asm volatile("bar.sync 1, 128;" ::: "memory");   // every row's note on V is in
+    const bool fix = flags[1] != 0;
+    const bool whole = a.n_splits == 1 || all <= a.tps;
+    const int head = n.h * a.G + (r - ri * a.G);
+    const int64_t row = (static_cast<int64_t>(n.q0) + tok) * a.Hq + head;
+    float* part = a.ws + ((static_cast<int64_t>(blockIdx.x) * a.n_splits + blockIdx.y) * kRows + r) *
+                             (D + 4);
+    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+      uint32_t o[32];
+      if (nt > 0) {
+        tc5::ld32(lanes + q * 32, o);
+        tc5::wait_ld32(o);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0;
+      }
+      if (!live) continue;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+      if (fix) {
+        for (int t = max(lim_min, j0 * NB); t < min(limit, j1 * NB); ++t) {
+          const uint16_t* vr = a.v + (n.k0 + t) * a.vs + static_cast<int64_t>(n.h) * D + q * 32;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float v = to_f<BF>(vr[i]);
+            if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+          }
+        }
+      }
+      if (whole) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + q * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack2<BF>(__uint_as_float(o[i * 8 + e * 2]), __uint_as_float(o[i * 8 + e * 2 + 1]));
+          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(part + q * 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[i] = make_uint4(o[i * 4], o[i * 4 + 1], o[i * 4 + 2], o[i * 4 + 3]);
+      }
+    }
+    if (live) {
+      if (whole) {
+        if (a.lse)
+          a.lse[row] = m == kNegInf ? kNegInf
+                                    : (m - tc5::kOff + log2f(l)) * 0.6931471805599453f;
+      } else {
+        part[D] = m;
+        part[D + 1] = l;
+      }
+    }
+    tc5::fence_before();
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 4) {
+    tc5::fence_after();
+    tc5::tmem_dealloc(tmem, L::kCols);
+  }
+  if (threadIdx.x == 0 && flags[0]) report(a.err, KVQ_DEVERR_TIMEOUT);
 }
 
-template <bool BF>
-void launch(const PromptArgs& a, int D, int blocks, cudaStream_t cs) {
-  if (D == 256) prompt_rows_kernel<BF, 256><<<blocks, 256, 0, cs>>>(a);
-  else if (D == 128) prompt_rows_kernel<BF, 128><<<blocks, 256, 0, cs>>>(a);
-  else prompt_rows_kernel<BF, 64><<<blocks, 256, 0, cs>>>(a);
+// Joins the splits of a row: one warp per row of a unit; lane holds D / 32 channels.
+template <bool BF, int D>
+__global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
+  constexpr int NB = Cfg<D>::NB, E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const Unit n = find_unit(a, blockIdx.x, false);
+  if (!n.found) return;
+  const int i0 = n.tile * a.tpt, i1 = min(i0 + a.tpt, n.lq);
+  const int all = (keys_seen(n, i1 - 1) + NB - 1) / NB;
+  if (all <= a.tps) return;
+  const int live = (all + a.tps - 1) / a.tps;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int tok = i0 + r / a.G;
+  if (r >= (i1 - i0) * a.G) return;
+  const float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * a.n_splits * kRows + r) * (D + 4);
+  constexpr int64_t step = static_cast<int64_t>(kRows) * (D + 4);
+  float M = kNegInf;
+  for (int i = lane; i < live; i += 32) M = fmaxf(M, part[i * step + D]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+  float O[E], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) O[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < live; ++i) {
+    const float* p = part + i * step;
+    const float mi = p[D], f = mi == kNegInf ? 0.f : ex2_fast(mi - M);
+    l = fmaf(p[D + 1], f, l);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 o = *reinterpret_cast<const float2*>(p + e * 32 + lane * 2);
+      O[e] = fmaf(o.x, f, O[e]);
+      O[e + 1] = fmaf(o.y, f, O[e + 1]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t row = (static_cast<int64_t>(n.q0) + tok) * a.Hq + n.h * a.G + r % a.G;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(a.out + row * D + e * 32 + lane * 2) =
+        pack2<BF>(O[e] * inv, O[e + 1] * inv);
+  if (a.lse && lane == 0)
+    a.lse[row] = M == kNegInf ? kNegInf : (M - tc5::kOff + log2f(l)) * 0.6931471805599453f;
+}
+
+// How a call is cut: row tiles (an upper bound: the lengths are on the device) and splits.
+struct Plan {
+  int tpt, tps, n_splits;
+  int64_t units;
+};
+
+Plan plan_for(int nseq, int total_q, int num_q_heads, int num_kv_heads, int D, int max_q,
+              int max_k) {
+  const int nb = D == 64 ? 64 : 128, ctas = D == 256 ? 1 : 2;
+  Plan p;
+  p.tpt = kRows / (num_q_heads / num_kv_heads);
+  const int64_t per = (static_cast<int64_t>(max_q) + p.tpt - 1) / p.tpt;
+  const int64_t a = static_cast<int64_t>(nseq) * per, b = total_q / p.tpt + static_cast<int64_t>(nseq);
+  p.units = (a < b ? a : b) * num_kv_heads;
+  const int tiles = (max_k + nb - 1) / nb;
+  const int64_t slots = static_cast<int64_t>(sm_count() > 0 ? sm_count() : 152) * ctas;
+  // Split only while the units leave SMs idle, and not below four tiles per split: a split costs
+  // its start (about the time of two tiles) and its partial rows.
+  int64_t want = p.units > 0 ? slots / p.units : 1;
+  const int64_t most = (tiles + 3) / 4;
+  want = want > most ? most : want;
+  if (want < 1) want = 1;
+  p.tps = static_cast<int>((tiles + want - 1) / want);
+  if (p.tps < 1) p.tps = 1;
+  p.n_splits = tiles > 0 ? (tiles + p.tps - 1) / p.tps : 1;
+  return p;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static std::mutex mu;
+  static EncodeFn fn = nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!fn) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &st) == cudaSuccess && st == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+  }
+  return fn;
+}
+
+// Rows [tokens][heads][D] in boxes of 64 channels x `bh` heads x `bt` tokens, 128-byte swizzle.
+bool encode(CUtensorMap* m, bool bf, const uint16_t* base, int64_t stride, int tokens, int heads,
+            int D, int bh, int bt) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(bh), static_cast<cuuint32_t>(bt)};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return encode_fn()(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                     const_cast<uint16_t*>(base), dims, strides, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF, int D>
+kvq_status launch(const char* fn, PromptArgs& a, const Plan& p, const uint16_t* q, int64_t qs,
+                  const uint16_t* k, int64_t ks, const uint16_t* v, int64_t vs, cudaStream_t cs) {
+  using C = Cfg<D>;
+  CUtensorMap mq, mk, mv;
+  if (!encode_fn()) return fail(KVQ_ERR_CUDA, "%s: the driver has no cuTensorMapEncodeTiled", fn);
+  bool ok = encode(&mq, BF, q, qs, a.total_q, a.Hq, D, a.G, p.tpt);
+  if (a.total_k > 0) {
+    ok = ok && encode(&mk, BF, k, ks, a.total_k, a.H, D, 1, C::NB) &&
+         encode(&mv, BF, v, vs, a.total_k, a.H, D, 1, C::VR);
+  } else {
+    mk = mv = mq;   // no key: no copy is issued
+  }
+  if (!ok) return fail(KVQ_ERR_CUDA, "%s: cuTensorMapEncodeTiled refused q, k or v", fn);
+  cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<BF, D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kTotal);
+  if (e == cudaSuccess) {
+    const dim3 grid(static_cast<unsigned>(p.units), p.n_splits);
+    prompt_attn_kernel<BF, D><<<grid, kThreads, Lay<D>::kTotal, cs>>>(a, mq, mk, mv);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && p.n_splits > 1) {
+    const int rows = a.G * (a.max_q < p.tpt ? a.max_q : p.tpt);
+    prompt_join_kernel<BF, D><<<dim3(static_cast<unsigned>(p.units), (rows + 7) / 8), 256, 0, cs>>>(a);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
+  return ok ? kvq::ok() : KVQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -99,10 +669,14 @@ void launch(const PromptArgs& a, int D, int blocks, cudaStream_t cs) {
 extern "C" size_t kvq_prompt_attn_workspace(int nseq, int total_q, int num_q_heads,
                                             int num_kv_heads, int head_dim, int max_q,
                                             int max_k) {
-  (void)head_dim;
-  if (nseq < 1 || total_q < 0 || num_q_heads < 1 || num_kv_heads < 1 || max_q < 0 || max_k < 0)
+  if (nseq < 1 || total_q < 0 || num_kv_heads < 1 || num_q_heads < num_kv_heads ||
+      num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > kvq::kRows || max_q < 0 ||
+      max_k < 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256))
     return 0;
-  return 16;
+  const kvq::Plan p =
+      kvq::plan_for(nseq, total_q, num_q_heads, num_kv_heads, head_dim, max_q, max_k);
+  if (p.n_splits == 1) return 16;
+  return static_cast<size_t>(p.units) * p.n_splits * kvq::kRows * (head_dim + 4) * sizeof(float);
 }
 
 extern "C" kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_t q_stride,
@@ -144,15 +718,25 @@ extern "C" kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_
                                                 head_dim, max_q, max_k);
   if (workspace_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
-  PromptArgs a{q, k, v, q_stride, k_stride, v_stride, cu_q, cu_k, out, lse, dev_err, nseq, total_q,
-               total_k, max_q, max_k, num_q_heads, num_kv_heads, softmax_scale};
-  const int64_t warps = static_cast<int64_t>(total_q) * num_q_heads;
-  const int64_t want = (warps + 7) / 8, cap = 152 * 8;
-  const int blocks = static_cast<int>(want < cap ? want : cap);
+  const Plan p = plan_for(nseq, total_q, num_q_heads, num_kv_heads, head_dim, max_q, max_k);
+  if (p.units > INT32_MAX)
+    return fail(KVQ_ERR_RANGE, "%s: %lld row tiles exceed the grid", fn,
+                static_cast<long long>(p.units));
+  PromptArgs a;
+  a.v = v; a.vs = v_stride; a.cu_q = cu_q; a.cu_k = cu_k; a.out = out; a.lse = lse;
+  a.ws = static_cast<float*>(workspace); a.err = dev_err; a.nseq = nseq; a.total_q = total_q;
+  a.total_k = total_k; a.max_q = max_q; a.max_k = max_k; a.Hq = num_q_heads; a.H = num_kv_heads;
+  a.G = num_q_heads / num_kv_heads; a.tpt = p.tpt; a.n_splits = p.n_splits; a.tps = p.tps;
+  a.c = softmax_scale * 1.4426950408889634f;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == KVQ_BF16) launch<true>(a, head_dim, blocks, cs);
-  else launch<false>(a, head_dim, blocks, cs);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
-  return ok();
+  auto go = [&](auto bf, auto d) {
+    return launch<decltype(bf)::value, decltype(d)::value>(fn, a, p, q, q_stride, k, k_stride, v,
+                                                           v_stride, cs);
+  };
+  auto by_dim = [&](auto bf) {
+    if (head_dim == 256) return go(bf, std::integral_constant<int, 256>());
+    if (head_dim == 128) return go(bf, std::integral_constant<int, 128>());
+    return go(bf, std::integral_constant<int, 64>());
+  };
+  return dtype == KVQ_BF16 ? by_dim(std::true_type()) : by_dim(std::false_type());
 }
