@@ -468,6 +468,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
 #pragma unroll 1
     for (int q = 0; q < D / 32; ++q) {
       uint32_t o[32];
+      __syncwarp();
       if (nt > 0) {
         tc5::ld32(lanes + q * 32, o);
         tc5::wait_ld32(o);

@@ -1,4 +1,28 @@
-// Attention of drafted tokens over the packed pages: one warp per (layer, node, query head).
+// Attention of a tree of drafted tokens over the packed pages, on the fifth-generation tensor
+// cores.
+//
+// The rows of a tile are (draft, grouped query head) pairs of one KV head, 128 at most; per tile
+// of 64 tokens the packed codes are brought in once and become fp16 in shared memory, exactly as
+// the dequantizer rounds them (k_hat = fp16(c * scale)):
+//   S = Q K_hat^T       tcgen05.mma, Q (fp16) in TMEM, K_hat in shared memory
+//   p = 2^(S c - m)     one thread per row, running maximum and sum; drafts outside the row's
+//                       64-bit ancestor mask get weight 0
+//   O += P V_hat        tcgen05.mma, P (fp16) in TMEM over the place of S, V_hat in shared memory
+// TMEM is full: O 256 columns, two score buffers of 64, Q 128.  With Q in TMEM the first product
+// reads only K_hat from shared memory, whose bandwidth is the scarcest after the codes' arrival.
+//
+// Roles of the 14 warps of a persistent CTA (one per SM): 4 softmax, 1 issues the products, 1
+// issues bulk copies of codes and scales (16-token groups of a page) into a ring deep enough to
+// cover the memory latency, 8 unpack.
+//
+// Work: the tiles of all (layer, sequence, KV head, row tile) units in one line are dealt to the
+// CTAs in equal contiguous shares, whatever the sequences' lengths (which only the device knows).
+// A unit that lies inside one share is finished there; the at most two cut units of a share leave
+// (m, l, O) and a second kernel joins them.  Short caches (8 tiles at most) are dealt whole units.
+//
+// Order of channels: unpacking is cheapest when it leaves pairs that lie 16 bits apart, so K_hat,
+// V_hat and Q hold the channels of each group of 4 (q6) or 8 (q4) permuted; scores do not change,
+// and O's columns are put back in order when they are stored.
 #include <cmath>
 #include <cstdint>
 
@@ -7,11 +31,25 @@
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "kvq_math.cuh"
+#include "kvq_tc5.cuh"
 
 namespace kvq {
 namespace {
 
+#define kNegInf (-__int_as_float(0x7f800000))
+
 constexpr int kD = 256;
+constexpr int kRows = 128;
+constexpr int kTile = 64;             // tokens per tile
+constexpr int kSoftmaxThreads = 128;  // warps 0-3
+constexpr int kMmaWarp = 4, kCopyWarp = 5, kUnpackWarp0 = 6, kUnpackWarps = 8;
+constexpr int kThreads = (kUnpackWarp0 + kUnpackWarps) * 32;
+constexpr int kRec = kD + 4;          // a partial row: O[256], m, l, pad, pad
+constexpr int kShortTiles = 8;        // caches of at most so many tiles are not cut
+constexpr int kMeta = 16;             // entries of the ring of group-validity bits
+constexpr int kStage = kTile * kD * 2;
+constexpr uint32_t kColS = 256, kColQ = 384, kCols = 512;   // TMEM: O at 0, S at 256 and 320, Q
 
 struct TreePools {
   const uint8_t* kc;
@@ -25,17 +63,231 @@ struct TreeArgs {
   TreePools L[KVQ_MAX_TENSORS];
   const uint16_t* q;
   uint16_t* out;
+  float* ws;
   const int32_t* pt;
   const int32_t* lens;
   const int32_t* cu;
   const int32_t* parents;
   int32_t* err;
-  int n_layers, nseq, total, H, Hq, ps, max_pages, max_nodes, max_len;
-  float scale;
+  int n_layers, nseq, total, H, Hq, G, ps, max_pages, max_nodes, max_len;
+  int tpt;      // drafts per row tile
+  int grid;     // CTAs of the attention kernel
+  int whole;    // deal whole units (short caches)
+  float c;      // softmax_scale * log2(e)
 };
 
 template <int BITS>
-__device__ __forceinline__ float value(const uint8_t* row, float sc, int d) {
+struct Lay {
+  static constexpr int kPd = kD * BITS / 8;
+  static constexpr int kRaw = 2 * kTile * kPd + 4 * kTile;   // K codes, V codes, K and V scales
+  static constexpr int kRaws = BITS == 8 ? 3 : BITS == 6 ? 4 : 6;
+  static constexpr int kK = 0, kV = 2 * kStage, kRawAt = 4 * kStage;
+  static constexpr int kBars = kRawAt + kRaws * kRaw;
+  static constexpr int kNumBars = 2 * kRaws + 4 * 2 + 3 * 2 + 2;
+  static constexpr int kTail = kBars + kNumBars * 8;         // then: TMEM address, flags, meta,
+  static constexpr int kParents = kTail + 16 + kMeta * 4;    // and the parents
+  static constexpr int kTotal = kParents + KVQ_MAX_NODES * 4;
+  static_assert(kTotal <= 232448, "shared memory");
+};
+
+// Where the element of natural index e of an aligned group of 8 channels is stored.
+template <int BITS> __host__ __device__ constexpr int place(int e) {
+  return BITS == 6 ? (e & 4) | ((e & 1) << 1) | ((e >> 1) & 1)
+         : BITS == 4 ? ((e & 3) << 1) | (e >> 2) : e;
+}
+
+struct Seq {
+  int n0, n, len, tiles, rt;   // first draft, drafts, cached tokens, token tiles, row tiles
+};
+
+__device__ __forceinline__ Seq seq_of(const TreeArgs& a, int s, bool check) {
+  Seq q{0, 0, 0, 0, 0};
+  if (s >= a.nseq) return q;
+  const int n0 = __ldg(a.cu + s), n1 = __ldg(a.cu + s + 1), len = __ldg(a.lens + s);
+  if (n0 >= 0 && n1 >= n0 && n1 <= a.total && n1 - n0 <= a.max_nodes && len >= 0 &&
+      static_cast<int64_t>(len) + (n1 - n0) <= a.max_len) {
+    q.n0 = n0;
+    q.n = n1 - n0;
+    q.len = len;
+    if (q.n > 0) {
+      q.tiles = (len + q.n + kTile - 1) / kTile;
+      q.rt = (q.n + a.tpt - 1) / a.tpt;
+    }
+  } else if (check) {
+    report(a.err, KVQ_DEVERR_INDEX);
+  }
+  return q;
+}
+
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(kFullMask, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Tiles and units of one layer (whole warp).
+__device__ __forceinline__ void layer_totals(const TreeArgs& a, bool check, int64_t& tiles,
+                                             int64_t& units) {
+  const int lane = threadIdx.x & 31;
+  int64_t t = 0, u = 0;
+  for (int s = lane; s < a.nseq; s += 32) {
+    const Seq q = seq_of(a, s, check);
+    u += static_cast<int64_t>(q.rt) * a.H;
+    t += static_cast<int64_t>(q.rt) * a.H * q.tiles;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    t += __shfl_xor_sync(kFullMask, t, o);
+    u += __shfl_xor_sync(kFullMask, u, o);
+  }
+  tiles = t;
+  units = u;
+}
+
+struct Unit {
+  Seq q;
+  int l, s, h, r;    // layer, sequence, KV head, row tile
+  int tile;          // the tile sought
+  int64_t start;     // the unit's first tile in the line of all tiles
+};
+
+// The unit that holds tile `at` of the line of all tiles (BY_TILE), or unit number `at`; whole
+// warp, `at` in range.
+template <bool BY_TILE>
+__device__ __forceinline__ Unit find_unit(const TreeArgs& a, int64_t at, int64_t layer_tiles,
+                                          int64_t layer_units) {
+  const int lane = threadIdx.x & 31;
+  Unit r;
+  const int64_t per = BY_TILE ? layer_tiles : layer_units;
+  r.l = static_cast<int>(at / per);
+  const int64_t x = at - r.l * per;
+  int64_t before = 0, tiles_before = 0;
+  for (int base = 0; base < a.nseq; base += 32) {
+    const Seq q = seq_of(a, base + lane, false);
+    const int64_t units = static_cast<int64_t>(q.rt) * a.H, tiles = units * q.tiles;
+    const int64_t mine = BY_TILE ? tiles : units;
+    const int64_t incl = warp_scan(mine), tincl = BY_TILE ? incl : warp_scan(tiles);
+    const int64_t start = before + incl - mine;
+    const unsigned hit = __ballot_sync(kFullMask, x >= start && x < start + mine);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      r.s = base + src;
+      r.q.n0 = __shfl_sync(kFullMask, q.n0, src);
+      r.q.n = __shfl_sync(kFullMask, q.n, src);
+      r.q.len = __shfl_sync(kFullMask, q.len, src);
+      r.q.tiles = __shfl_sync(kFullMask, q.tiles, src);
+      r.q.rt = __shfl_sync(kFullMask, q.rt, src);
+      const int64_t rem = x - __shfl_sync(kFullMask, start, src);
+      const int64_t tstart = tiles_before + __shfl_sync(kFullMask, tincl - tiles, src);
+      const int64_t u = BY_TILE ? rem / r.q.tiles : rem;
+      r.tile = BY_TILE ? static_cast<int>(rem - u * r.q.tiles) : 0;
+      r.h = static_cast<int>(u / r.q.rt);
+      r.r = static_cast<int>(u - static_cast<int64_t>(r.h) * r.q.rt);
+      r.start = r.l * layer_tiles + tstart + u * r.q.tiles;
+      return r;
+    }
+    before += __shfl_sync(kFullMask, incl, 31);
+    tiles_before += __shfl_sync(kFullMask, tincl, 31);
+  }
+  r.s = -1;   // not reached for `at` in range
+  return r;
+}
+
+// A CTA's way through its share: segments (a unit's consecutive tiles).  Every role walks it.
+struct Walk {
+  int64_t at, end, step, layer_tiles, layer_units;
+  bool whole;
+};
+
+__device__ __forceinline__ int64_t share_of(const TreeArgs& a, int64_t layer_tiles) {
+  const int64_t all = layer_tiles * a.n_layers;
+  return (all + a.grid - 1) / a.grid;
+}
+
+__device__ __forceinline__ Walk walk_of(const TreeArgs& a, bool check) {
+  Walk w;
+  layer_totals(a, check, w.layer_tiles, w.layer_units);
+  w.whole = a.whole != 0;
+  if (w.whole) {
+    w.at = blockIdx.x;
+    w.end = w.layer_units * a.n_layers;
+    w.step = a.grid;
+  } else {
+    const int64_t share = share_of(a, w.layer_tiles), all = w.layer_tiles * a.n_layers;
+    w.at = min(all, share * blockIdx.x);
+    w.end = min(all, w.at + share);
+    w.step = 0;
+  }
+  return w;
+}
+
+struct Segment {
+  Unit u;
+  int count;   // tiles, from u.tile on
+};
+
+__device__ __forceinline__ bool next_segment(const TreeArgs& a, Walk& w, Segment& g) {
+  if (w.at >= w.end) return false;
+  if (w.whole) {
+    g.u = find_unit<false>(a, w.at, w.layer_tiles, w.layer_units);
+    g.count = g.u.q.tiles;
+    w.at += w.step;
+  } else {
+    g.u = find_unit<true>(a, w.at, w.layer_tiles, w.layer_units);
+    g.count = static_cast<int>(min(static_cast<int64_t>(g.u.q.tiles - g.u.tile), w.end - w.at));
+    w.at += g.count;
+  }
+  return g.u.s >= 0;
+}
+
+// 16 codes of a row (2 * BITS bytes at `src`, shared memory) times its scale, as two 16-byte
+// pieces in the stored order of channels.
+template <int BITS>
+__device__ __forceinline__ void unpack16(const unsigned char* src, uint32_t scale2, uint32_t o[8]) {
+  if constexpr (BITS == 8) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = w[i] ^ 0x80808080u;   // c + 128
+      o[2 * i] = hmul2u(hfma2u(prmt(u, 0x64646464u, 0x4140), kH1, kHm1152), scale2);
+      o[2 * i + 1] = hmul2u(hfma2u(prmt(u, 0x64646464u, 0x4342), kH1, kHm1152), scale2);
+    }
+  } else if constexpr (BITS == 6) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(src);
+    const uint32_t w0 = p[0], w1 = p[1], w2 = p[2];
+    // per group of 4: low half bytes 0-1 (u0 at bit 0, u1 at 6), high half bytes 1-2 (u2 at 4,
+    // u3 at 10): the mask leaves (u0, 16 u2), and after a shift by 6 (u1, 16 u3)
+    const uint32_t x[4] = {prmt(w0, w0, 0x2110), prmt(w0, w1, 0x5443), prmt(w1, w2, 0x4332),
+                           prmt(w2, w2, 0x3221)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = (x[i] & 0x03F0003Fu) | 0x64006400u;
+      const uint32_t b = ((x[i] >> 6) & 0x03F0003Fu) | 0x64006400u;
+      o[2 * i] = hmul2u(hfma2u(a, 0x2C003C00u, 0xD600E420u), scale2);
+      o[2 * i + 1] = hmul2u(hfma2u(b, 0x2C003C00u, 0xD600E420u), scale2);
+    }
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(src);
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t y = w[i] >> 8;
+      o[4 * i] = hmul2u(hfma2u((w[i] & 0x000F000Fu) | 0x64006400u, kH1, kHm1032), scale2);
+      o[4 * i + 1] = hmul2u(hfma2u((w[i] & 0x00F000F0u) | 0x64006400u, kH16th, kHm72), scale2);
+      o[4 * i + 2] = hmul2u(hfma2u((y & 0x000F000Fu) | 0x64006400u, kH1, kHm1032), scale2);
+      o[4 * i + 3] = hmul2u(hfma2u((y & 0x00F000F0u) | 0x64006400u, kH16th, kHm72), scale2);
+    }
+  }
+}
+
+// v_hat of channel d of a packed row in global memory (the rare path of non-finite drafts).
+template <int BITS>
+__device__ __forceinline__ float value_at(const uint8_t* row, float sc, int d) {
   int c;
   if constexpr (BITS == 8) {
     c = static_cast<int8_t>(row[d]);
@@ -43,74 +295,511 @@ __device__ __forceinline__ float value(const uint8_t* row, float sc, int d) {
     c = static_cast<int>((row[d >> 1] >> ((d & 1) * 4)) & 15) - 8;
   } else {
     const uint8_t* b = row + d / 4 * 3;
-    const uint32_t w = b[0] | (b[1] << 8) | (b[2] << 16);
-    c = static_cast<int>((w >> (6 * (d & 3))) & 63u) - 32;
+    c = static_cast<int>(((b[0] | (b[1] << 8) | (b[2] << 16)) >> (6 * (d & 3))) & 63u) - 32;
   }
   return h2f(f2h(static_cast<float>(c) * sc));
 }
 
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
+                                          const volatile int* gave_up) {
+  return __all_sync(kFullMask, tc5::wait(bar, parity, gave_up));
+}
+
 template <int BITS>
-__global__ void __launch_bounds__(256) tree_rows_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int PD = kD * BITS / 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t n_rows = static_cast<int64_t>(a.n_layers) * a.total * a.Hq;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < n_rows;
-       row += step) {
-    const int j = static_cast<int>(row % a.Hq);
-    const int t = static_cast<int>(row / a.Hq % a.total);
-    const TreePools& P = a.L[row / a.Hq / a.total];
-    const int s = find_seq_from(a.cu, a.nseq, t, 0);
-    const int n0 = a.cu[s], n1 = a.cu[s + 1], len = a.lens[s];
-    if (t < n0 || t >= n1) continue;
-    if (n0 < 0 || n1 > a.total || n1 - n0 > a.max_nodes || len < 0 ||
-        static_cast<int64_t>(len) + n1 - n0 > a.max_len) {
-      report(a.err, KVQ_DEVERR_INDEX);
-      continue;
+__global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_constant__ TreeArgs a) {
+  using L = Lay<BITS>;
+  constexpr int R = L::kRaws;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
+  uint64_t *rawfull = bars, *rawempty = bars + R, *kfull = bars + 2 * R, *kempty = kfull + 2,
+           *vfull = kempty + 2, *vempty = vfull + 2, *sfull = vempty + 2, *pready = sfull + 2,
+           *odone = pready + 2, *qready = odone + 2, *drain = qready + 1;
+  uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::kTail);
+  volatile int* flags = reinterpret_cast<volatile int*>(tmem_ptr + 1);   // [0] gave up, [1] V
+  volatile int* meta = reinterpret_cast<volatile int*>(sm + L::kTail + 16);
+  int* parents = reinterpret_cast<int*>(sm + L::kParents);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Walk w = walk_of(a, blockIdx.x == 0 && warp == 0);
+  if (w.at >= w.end) return;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R; ++i) { mbar_init(rawfull + i, 1); mbar_init(rawempty + i, kUnpackWarps); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kfull + i, kUnpackWarps);
+      mbar_init(kempty + i, 1);
+      mbar_init(vfull + i, kUnpackWarps);
+      mbar_init(vempty + i, 1);
+      mbar_init(sfull + i, 1);
+      mbar_init(pready + i, kSoftmaxThreads);
+      mbar_init(odone + i, 1);
     }
-    uint64_t seen = 0;
-    for (int i = t - n0; i >= 0;) {
-      seen |= 1ull << i;
-      int p = a.parents[n0 + i];
-      if (p < -1 || p >= i) {
-        report(a.err, KVQ_DEVERR_INDEX);
-        p = -1;
-      }
-      i = p;
-    }
-    const int h = j / (a.Hq / a.H);
-    float qf[8], o[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      qf[e] = h2f(a.q[row * kD + lane * 8 + e]);
-      o[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < len + n1 - n0; ++i) {
-      if (i >= len && !((seen >> (i - len)) & 1)) continue;
-      const int64_t kr = locate_row(a.pt, a.max_pages, a.ps, a.H, P.k_pages, s, i, h, a.err);
-      const int64_t vr = locate_row(a.pt, a.max_pages, a.ps, a.H, P.v_pages, s, i, h, a.err);
-      if (kr < 0 || vr < 0) continue;
-      const float ks = h2f(P.ks[kr]), vs = h2f(P.vs[vr]);
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x = fmaf(qf[e], value<BITS>(P.kc + kr * PD, ks, lane * 8 + e), x);
-#pragma unroll
-      for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(kFullMask, x, w);
-      x *= a.scale;
-      const float mn = fmaxf(m, x);
-      const float f = m == -INFINITY ? 0.f : expf(m - mn), p = expf(x - mn);
-      l = l * f + p;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[e] = o[e] * f + p * value<BITS>(P.vc + vr * PD, vs, lane * 8 + e);
-      m = mn;
-    }
-    const float inv = m > -INFINITY ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a.out[row * kD + lane * 8 + e] = f2h(o[e] * inv);
+    mbar_init(qready, kSoftmaxThreads);
+    mbar_init(drain, 1);
+    tc5::fence_barrier_init();
+    flags[0] = 0;
+    flags[1] = 0;
   }
+  if (warp == kMmaWarp) tc5::tmem_alloc(tmem_ptr, kCols);
+  tc5::fence_before();
+  __syncthreads();
+  tc5::fence_after();
+  const uint32_t tmem = *tmem_ptr;
+  Segment g;
+  int it = 0;        // tiles done by this CTA
+  bool ok = true;
+
+  if (warp == kCopyWarp) {
+    // ------------------------------------------------------------------------- bulk copies
+    // Lane i looks up the page of 16-token group i of the next 8 tiles; then lanes 0-3 bring in
+    // each tile's four groups.
+    while (ok && next_segment(a, w, g)) {
+      const TreePools& P = a.L[g.u.l];
+      const int total = g.u.q.len + g.u.q.n;
+      for (int b = 0; ok && b < g.count; b += 8) {
+        const int tg = (g.u.tile + b) * kTile + lane * 16;
+        int64_t row = -1;
+        if (b * 4 + lane < g.count * 4 && tg < total) {
+          const int lp = tg / a.ps;
+          const int page = lp < a.max_pages
+                               ? __ldg(a.pt + static_cast<int64_t>(g.u.s) * a.max_pages + lp) : -1;
+          if (page >= 0 && page < P.k_pages && page < P.v_pages)
+            row = (static_cast<int64_t>(page) * a.H + g.u.h) * a.ps + (tg - lp * a.ps);
+          else
+            report(a.err, KVQ_DEVERR_PAGE_RANGE);
+        }
+        for (int j = 0; j < 8 && b + j < g.count; ++j, ++it) {
+          const int64_t r = __shfl_sync(kFullMask, row, j * 4 + (lane & 3));
+          const int st = it % R;
+          if (it >= R) ok = warp_wait(rawempty + st, (it / R + 1) & 1, flags);
+          if (!ok) break;
+          const unsigned have = __ballot_sync(kFullMask, lane < 4 && r >= 0);
+          if (lane == 0) {
+            meta[it % kMeta] = static_cast<int>(have);
+            mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd + 64));
+          }
+          __syncwarp();
+          if (lane < 4 && r >= 0) {
+            unsigned char* dst = sm + L::kRawAt + st * L::kRaw;
+            bulk_g2s(dst + lane * 16 * L::kPd, P.kc + r * L::kPd, 16 * L::kPd, rawfull + st);
+            bulk_g2s(dst + (kTile + lane * 16) * L::kPd, P.vc + r * L::kPd, 16 * L::kPd,
+                     rawfull + st);
+            bulk_g2s(dst + 2 * kTile * L::kPd + lane * 32, P.ks + r, 32, rawfull + st);
+            bulk_g2s(dst + 2 * kTile * L::kPd + 2 * kTile + lane * 32, P.vs + r, 32, rawfull + st);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (!ok) {   // wait for the copies in flight
+      for (int i = max(0, it - R); i < it; ++i) mbar_wait_bounded(rawfull + i % R, (i / R) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- products (one thread)
+    const uint32_t base = smem_u32(sm);
+    const uint64_t dk = tc5::desc_base(16), dv = tc5::desc_base(kTile * 128);
+    constexpr uint32_t id_s = tc5::idesc(false, kTile, false), id_o = tc5::idesc(false, kD, true);
+    int seg = 0;
+    while (ok && next_segment(a, w, g)) {
+      if (lane == 0) {
+        auto product_s = [&](int i) {
+          ok = ok && tc5::wait(kfull + (i & 1), (i >> 1) & 1, flags);
+          if (!ok) return;
+          tc5::fence_after();
+          const uint32_t kb = base + L::kK + (i & 1) * kStage;
+#pragma unroll
+          for (int k = 0; k < kD / 16; ++k)
+            tc5::mma_ts(tmem + kColS + (i & 1) * kTile, tmem + kColQ + k * 8,
+                        tc5::desc_at(dk, kb + (k / 4) * kTile * 128 + (k % 4) * 32), id_s, k > 0);
+          tc5::commit(kempty + (i & 1));
+          tc5::commit(sfull + (i & 1));
+        };
+        auto product_o = [&](int i, bool first) {
+          ok = ok && tc5::wait(vfull + (i & 1), (i >> 1) & 1, flags);
+          ok = ok && tc5::wait(pready + (i & 1), (i >> 1) & 1, flags);
+          if (!ok) return;
+          tc5::fence_after();
+          const uint32_t vb = base + L::kV + (i & 1) * kStage;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            tc5::mma_ts(tmem, tmem + kColS + (i & 1) * kTile + k * 8,
+                        tc5::desc_at(dv, vb + k * 2048), id_o, !first || k > 0);
+          tc5::commit(vempty + (i & 1));
+          tc5::commit(odone + (i & 1));
+        };
+        ok = tc5::wait(qready, seg & 1, flags);
+        tc5::fence_after();
+        if (ok) product_s(it);
+        for (int j = 0; ok && j < g.count; ++j) {
+          // the next scores go over the weights of the tile before this one, whose product was
+          // issued earlier: products of one CTA run in the order of their issue
+          if (j + 1 < g.count) product_s(it + j + 1);
+          if (ok) product_o(it + j, j == 0);
+        }
+      }
+      ok = __shfl_sync(kFullMask, ok, 0);
+      it += g.count;
+      ++seg;
+    }
+    if (!ok) {   // what was issued must end before the memory is given back
+      flags[0] = 1;
+      if (lane == 0) {
+        tc5::commit(drain);
+        mbar_wait_bounded(drain, 0);
+      }
+    }
+  } else if (warp >= kUnpackWarp0) {
+    // ------------------------------------------------------------------------------- unpack
+    // A warp's step takes two rows: lanes 8q .. 8q+7 hold panel q (64 channels) of both, four
+    // 16-channel units each, which spreads a quarter-warp's 16-byte stores over all banks.
+    const int q = lane >> 3, rr = (lane >> 2) & 1, u = lane & 3;
+    const int src = (q * 4 + u) * 2 * BITS;
+    while (ok && next_segment(a, w, g)) {
+      const int len = g.u.q.len, total = len + g.u.q.n;
+      for (int j = 0; j < g.count; ++j, ++it) {
+        const int st = it % R, t0 = (g.u.tile + j) * kTile;
+        ok = warp_wait(rawfull + st, (it / R) & 1, flags);
+        if (!ok) break;
+        const unsigned have = static_cast<unsigned>(meta[it % kMeta]);
+        const unsigned char* raw = sm + L::kRawAt + st * L::kRaw;
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(raw + 2 * kTile * L::kPd);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t* empty = (kv ? vempty : kempty) + (it & 1);
+          if (it >= 2) ok = warp_wait(empty, (it / 2 + 1) & 1, flags);
+          if (!ok) break;
+          unsigned char* dst = sm + (kv ? L::kV : L::kK) + (it & 1) * kStage + q * kTile * 128;
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < kTile / 2 / kUnpackWarps; ++i) {
+            const int row = (i * kUnpackWarps + warp - kUnpackWarp0) * 2 + rr;
+            // rows that are not there become zeros (a code is always finite)
+            const bool there = t0 + row < total && (have >> (row >> 4) & 1);
+            const uint32_t s1 = there ? sc[kv * kTile + row] : 0u;
+            uint32_t o[8];
+            unpack16<BITS>(raw + (kv * kTile + row) * L::kPd + src, s1 | (s1 << 16), o);
+            if (kv && t0 + kTile > len && t0 + row >= len) {
+              // a draft only some rows see: 0 * inf must not reach the others
+              bool bad = false;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) bad = bad || nonfinite2(o[e]);
+              if (bad) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  if ((o[e] & 0x7c00u) == 0x7c00u) o[e] &= 0xffff0000u;
+                  if ((o[e] & 0x7c000000u) == 0x7c000000u) o[e] &= 0x0000ffffu;
+                }
+                found = true;
+              }
+            }
+            unsigned char* p = dst + row * 128;
+            const int at = ((2 * u) ^ (row & 7)) * 16;
+            *reinterpret_cast<uint4*>(p + at) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(p + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
+          if (found) flags[1] = 1;
+          tc5::fence_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive((kv ? vfull : kfull) + (it & 1));
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(rawempty + st);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax: thread = row
+    const int r = threadIdx.x, ri = r / a.G;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
+    while (ok && next_segment(a, w, g)) {
+      const Seq& q = g.u.q;
+      const int node = g.u.r * a.tpt + ri;
+      const bool live = ri < a.tpt && node < q.n;
+      const int64_t row = (static_cast<int64_t>(g.u.l) * a.total + q.n0 + node) * a.Hq +
+                          g.u.h * a.G + (r - ri * a.G);
+      // Q of this row into TMEM, channels in the stored order
+#pragma unroll 1
+      for (int b = 0; b < kD / 64; ++b) {
+        uint32_t x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = ld_nc_v4(a.q + row * kD + b * 64 + i * 8);
+          if constexpr (BITS == 8) {
+            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+          } else if constexpr (BITS == 6) {
+            x[4 * i] = prmt(v.x, v.y, 0x5410);
+            x[4 * i + 1] = prmt(v.x, v.y, 0x7632);
+            x[4 * i + 2] = prmt(v.z, v.w, 0x5410);
+            x[4 * i + 3] = prmt(v.z, v.w, 0x7632);
+          } else {
+            x[4 * i] = prmt(v.x, v.z, 0x5410);
+            x[4 * i + 1] = prmt(v.x, v.z, 0x7632);
+            x[4 * i + 2] = prmt(v.y, v.w, 0x5410);
+            x[4 * i + 3] = prmt(v.y, v.w, 0x7632);
+          }
+        }
+        tc5::st32(lanes + kColQ + b * 32, x);
+      }
+      tc5::wait_st();
+      tc5::fence_before();
+      mbar_arrive(qready);
+      // the ancestors, if drafts are among this segment's tokens
+      uint64_t seen = 0;
+      const bool drafts = (g.u.tile + g.count) * kTile > q.len;
+      if (drafts) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");   // the previous unit's are no longer read
+        if (r < q.n) {
+          int p = __ldg(a.parents + q.n0 + r);
+          if (p < -1 || p >= r) {
+            report(a.err, KVQ_DEVERR_INDEX);
+            p = -1;
+          }
+          parents[r] = p;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (live)
+          for (int i = node; i >= 0; i = parents[i]) seen |= 1ull << i;
+      }
+      float m = kNegInf, l = 0.f;
+      for (int j = 0; j < g.count; ++j, ++it) {
+        ok = warp_wait(sfull + (it & 1), (it >> 1) & 1, flags);
+        if (!ok) break;
+        tc5::fence_after();
+        const uint32_t sb = lanes + kColS + (it & 1) * kTile;
+        const int t0 = (g.u.tile + j) * kTile;
+        uint32_t s[kTile];
+        tc5::ld32(sb, s);
+        tc5::ld32(sb + 32, s + 32);
+        const unsigned have = static_cast<unsigned>(meta[it % kMeta]);
+        tc5::wait_ld32(s);
+        tc5::after_ld32(s + 32);
+        if (t0 + kTile > q.len || have != 15u) {
+          const int d0 = t0 - q.len;   // node number of the tile's first token
+          uint64_t vis = d0 >= 0 ? (d0 < 64 ? seen >> d0 : 0)
+                       : d0 > -64 ? (seen << -d0) | ((1ull << -d0) - 1) : ~0ull;
+#pragma unroll
+          for (int gi = 0; gi < 4; ++gi)
+            if (!(have >> gi & 1)) vis &= ~(0xffffull << (16 * gi));
+          const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (!(v0 >> i & 1)) s[i] = 0xff800000u;
+            if (!(v1 >> i & 1)) s[32 + i] = 0xff800000u;
+          }
+        }
+        float mx0 = kNegInf, mx1 = kNegInf, mx2 = kNegInf, mx3 = kNegInf;
+#pragma unroll
+        for (int i = 0; i < kTile; i += 4) {
+          mx0 = fmaxf(mx0, __uint_as_float(s[i]));
+          mx1 = fmaxf(mx1, __uint_as_float(s[i + 1]));
+          mx2 = fmaxf(mx2, __uint_as_float(s[i + 2]));
+          mx3 = fmaxf(mx3, __uint_as_float(s[i + 3]));
+        }
+        const float x = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.c;
+        if (j == 0) {
+          m = x;
+        } else {
+          const bool up = x > m + tc5::kSlack;
+          if (__any_sync(kFullMask, up)) {
+            const float f = up ? ex2_fast(m - x) : 1.f;
+            if (up) m = x;
+            l *= f;
+            ok = warp_wait(odone + ((it - 1) & 1), (it - 1) >> 1 & 1, flags);
+            if (!ok) break;
+            tc5::fence_after();
+#pragma unroll 1
+            for (int b = 0; b < kD / 32; ++b) {
+              uint32_t o[32];
+              tc5::ld32(lanes + b * 32, o);
+              tc5::wait_ld32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tc5::st32(lanes + b * 32, o);
+            }
+            tc5::wait_st();
+          }
+        }
+        const float mo = m == kNegInf ? 0.f : m - tc5::kOff;
+        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float p0 = ex2_fast(fmaf(__uint_as_float(s[b * 32 + i]), a.c, -mo));
+            const float p1 = ex2_fast(fmaf(__uint_as_float(s[b * 32 + i + 1]), a.c, -mo));
+            const float p2 = ex2_fast(fmaf(__uint_as_float(s[b * 32 + i + 2]), a.c, -mo));
+            const float p3 = ex2_fast(fmaf(__uint_as_float(s[b * 32 + i + 3]), a.c, -mo));
+            l0 += p0; l1 += p1; l2 += p2; l3 += p3;
+            p[i / 2] = pack_h2(p0, p1);
+            p[i / 2 + 1] = pack_h2(p2, p3);
+          }
+          tc5::st16(sb + b * 16, p);
+        }
+        l += (l0 + l1) + (l2 + l3);
+        tc5::wait_st();
+        tc5::fence_before();
+        mbar_arrive(pready + (it & 1));
+      }
+      if (!ok) break;
+      ok = warp_wait(odone + ((it - 1) & 1), (it - 1) >> 1 & 1, flags);
+      if (!ok) break;
+      tc5::fence_after();
+      const bool whole = g.count == q.tiles;
+      const bool fix = drafts && flags[1] != 0;
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      // a cut unit at the head of the share is its first record, one at the tail its second
+      float* part = a.ws + ((static_cast<int64_t>(blockIdx.x) * 2 + (g.u.tile > 0 ? 0 : 1)) * kRows +
+                            r) * kRec;
+#pragma unroll 1
+      for (int b = 0; b < kD / 32; ++b) {
+        uint32_t o[32];
+        __syncwarp();
+        tc5::ld32(lanes + b * 32, o);
+        tc5::wait_ld32(o);
+        if (!live) continue;
+        uint32_t x[32];   // in natural order
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          x[i] = __float_as_uint(__uint_as_float(o[(i & ~7) | place<BITS>(i & 7)]) * inv);
+        if (fix) {
+          const TreePools& P = a.L[g.u.l];
+          const int lo = max(0, g.u.tile * kTile - q.len);
+          const int hi = min(q.n, (g.u.tile + g.count) * kTile - q.len);
+          for (int d = lo; d < hi; ++d) {
+            if (!(seen >> d & 1)) continue;
+            const int64_t at = locate_row(a.pt, a.max_pages, a.ps, a.H, P.v_pages, g.u.s,
+                                          static_cast<int64_t>(q.len) + d, g.u.h, nullptr);
+            if (at < 0) continue;
+            const float vs = h2f(P.vs[at]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float v = value_at<BITS>(P.vc + at * L::kPd, vs, b * 32 + i);
+              if (!isfinite(v)) x[i] = __float_as_uint(__uint_as_float(x[i]) + v);
+            }
+          }
+        }
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * kD + b * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = pack_h2(__uint_as_float(x[i * 8 + e * 2]), __uint_as_float(x[i * 8 + e * 2 + 1]));
+            dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(part + b * 32);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+      }
+      if (live && !whole) {
+        part[kD] = m;
+        part[kD + 1] = l;
+      }
+      tc5::fence_before();
+    }
+    if (!ok) flags[0] = 1;
+  }
+  if (!ok) flags[0] = 1;
+  __syncwarp();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc5::fence_after();
+    tc5::tmem_dealloc(tmem, kCols);
+  }
+  if (threadIdx.x == 0 && flags[0]) report(a.err, KVQ_DEVERR_TIMEOUT);
+}
+
+// Joins the records of a cut unit: one warp per row.
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  const int lane = threadIdx.x & 31;
+  int64_t tiles, units;
+  layer_totals(a, false, tiles, units);
+  if (blockIdx.x >= units * a.n_layers) return;
+  const Unit u = find_unit<false>(a, blockIdx.x, tiles, units);
+  if (u.s < 0) return;
+  const int64_t share = share_of(a, tiles);
+  const int c0 = static_cast<int>(u.start / share);
+  const int c1 = static_cast<int>((u.start + u.q.tiles - 1) / share);
+  if (c0 == c1) return;   // finished by its CTA
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int ri = r / a.G, node = u.r * a.tpt + ri;
+  if (ri >= a.tpt || node >= u.q.n) return;
+  auto rec = [&](int c) {   // the unit's start lies in c0's share, so there it is the tail
+    return a.ws + ((static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRows + r) * kRec;
+  };
+  float M = kNegInf;
+  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, rec(c)[kD]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+  float O[8], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) O[e] = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float* p = rec(c);
+    const float mi = p[kD], f = mi == kNegInf ? 0.f : ex2_fast(mi - M);
+    l = fmaf(p[kD + 1], f, l);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float4 o = *reinterpret_cast<const float4*>(p + e * 128 + lane * 4);
+      O[4 * e] = fmaf(o.x, f, O[4 * e]);
+      O[4 * e + 1] = fmaf(o.y, f, O[4 * e + 1]);
+      O[4 * e + 2] = fmaf(o.z, f, O[4 * e + 2]);
+      O[4 * e + 3] = fmaf(o.w, f, O[4 * e + 3]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t row = (static_cast<int64_t>(u.l) * a.total + u.q.n0 + node) * a.Hq + u.h * a.G +
+                      (r - ri * a.G);
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    *reinterpret_cast<uint2*>(a.out + row * kD + e * 128 + lane * 4) =
+        make_uint2(pack_h2(O[4 * e] * inv, O[4 * e + 1] * inv),
+                   pack_h2(O[4 * e + 2] * inv, O[4 * e + 3] * inv));
+}
+
+// How a call is cut; the units are an upper bound (the lengths are on the device).
+struct Plan {
+  int tpt, grid;
+  bool whole;
+  int64_t units;
+};
+
+Plan plan_for(int n_layers, int nseq, int total_nodes, int H, int Hq, int max_nodes, int max_len) {
+  Plan p;
+  p.tpt = kRows / (Hq / H);
+  const int64_t per = (max_nodes + p.tpt - 1) / p.tpt;
+  const int64_t a = static_cast<int64_t>(nseq) * per, b = total_nodes / p.tpt + static_cast<int64_t>(nseq);
+  p.units = (a < b ? a : b) * H * n_layers;
+  const int64_t tiles = (static_cast<int64_t>(max_len) + kTile - 1) / kTile;
+  p.whole = tiles <= kShortTiles;
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  const int64_t work = p.whole ? p.units : p.units * tiles;
+  p.grid = static_cast<int>(work < sms ? (work < 1 ? 1 : work) : sms);
+  return p;
+}
+
+template <int BITS>
+cudaError_t launch(const TreeArgs& a, const Plan& p, cudaStream_t cs) {
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<BITS>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Lay<BITS>::kTotal);
+  if (e != cudaSuccess) return e;
+  tree_attn_kernel<BITS><<<p.grid, kThreads, Lay<BITS>::kTotal, cs>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.whole) return e;
+  const int rows = a.G * (a.max_nodes < p.tpt ? a.max_nodes : p.tpt);
+  tree_join_kernel<<<dim3(static_cast<unsigned>(p.units), (rows + 7) / 8), 256, 0, cs>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -119,11 +808,16 @@ __global__ void __launch_bounds__(256) tree_rows_kernel(const __grid_constant__ 
 extern "C" size_t kvq_tree_attn_workspace(int n_layers, int nseq, int total_nodes,
                                           int num_kv_heads, int num_q_heads, int head_dim,
                                           int max_nodes, int max_seq_len) {
-  (void)head_dim; (void)max_nodes;
-  if (n_layers < 1 || nseq < 1 || total_nodes < 0 || num_kv_heads < 1 || num_q_heads < 1 ||
+  (void)head_dim;
+  if (n_layers < 1 || nseq < 1 || total_nodes < 0 || num_kv_heads < 1 ||
+      num_q_heads < num_kv_heads || num_q_heads % num_kv_heads ||
+      num_q_heads / num_kv_heads > kvq::kRows || max_nodes < 1 || max_nodes > KVQ_MAX_NODES ||
       max_seq_len < 0)
     return 0;
-  return 16;
+  const kvq::Plan p = kvq::plan_for(n_layers, nseq, total_nodes, num_kv_heads, num_q_heads,
+                                    max_nodes, max_seq_len);
+  if (p.whole) return 16;
+  return static_cast<size_t>(p.grid) * 2 * kvq::kRows * kvq::kRec * sizeof(float);
 }
 
 extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_pools, int n_layers,
@@ -172,25 +866,25 @@ extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_p
                                               max_nodes, max_seq_len);
   if (workspace_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
+  const Plan p = plan_for(n_layers, nseq, total_nodes, H, num_q_heads, max_nodes, max_seq_len);
+  if (p.units > INT32_MAX)
+    return fail(KVQ_ERR_RANGE, "%s: %lld row tiles exceed the grid", fn,
+                static_cast<long long>(p.units));
   TreeArgs a;
   for (int i = 0; i < KVQ_MAX_TENSORS; ++i)
     a.L[i] = i < n_layers ? TreePools{k_pools[i].codes, k_pools[i].scales, v_pools[i].codes,
                                       v_pools[i].scales, k_pools[i].num_pages,
                                       v_pools[i].num_pages}
                           : TreePools{nullptr, nullptr, nullptr, nullptr, 0, 0};
-  a.q = q; a.out = out; a.pt = page_table; a.lens = seq_lens; a.cu = cu_nodes;
-  a.parents = parents; a.err = dev_err; a.n_layers = n_layers; a.nseq = nseq;
-  a.total = total_nodes; a.H = H; a.Hq = num_q_heads; a.ps = k0.page_size;
-  a.max_pages = max_pages; a.max_nodes = max_nodes; a.max_len = max_seq_len;
-  a.scale = softmax_scale;
-  const int64_t warps = static_cast<int64_t>(n_layers) * total_nodes * num_q_heads;
-  const int64_t want = (warps + 7) / 8, cap = 152 * 8;
-  const int blocks = static_cast<int>(want < cap ? want : cap);
+  a.q = q; a.out = out; a.ws = static_cast<float*>(workspace); a.pt = page_table;
+  a.lens = seq_lens; a.cu = cu_nodes; a.parents = parents; a.err = dev_err;
+  a.n_layers = n_layers; a.nseq = nseq; a.total = total_nodes; a.H = H; a.Hq = num_q_heads;
+  a.G = num_q_heads / H; a.ps = k0.page_size; a.max_pages = max_pages; a.max_nodes = max_nodes;
+  a.max_len = max_seq_len; a.tpt = p.tpt; a.grid = p.grid; a.whole = p.whole ? 1 : 0;
+  a.c = softmax_scale * 1.4426950408889634f;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (k0.bits == 8) tree_rows_kernel<8><<<blocks, 256, 0, cs>>>(a);
-  else if (k0.bits == 6) tree_rows_kernel<6><<<blocks, 256, 0, cs>>>(a);
-  else tree_rows_kernel<4><<<blocks, 256, 0, cs>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = k0.bits == 8 ? launch<8>(a, p, cs)
+                        : k0.bits == 6 ? launch<6>(a, p, cs) : launch<4>(a, p, cs);
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
   return ok();
 }
