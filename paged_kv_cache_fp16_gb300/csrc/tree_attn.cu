@@ -45,7 +45,7 @@ constexpr int kTile = 64;             // tokens per tile
 constexpr int kSoftmaxThreads = 128;  // warps 0-3
 constexpr int kMmaWarp = 4, kCopyWarp = 5, kUnpackWarp0 = 6, kUnpackWarps = 8;
 constexpr int kThreads = (kUnpackWarp0 + kUnpackWarps) * 32;
-constexpr int kRec = kD + 4;          // a partial row: O[256], m, l, pad, pad
+constexpr int kRec = (kD + 2) * kRows;   // a partial record: O [256][128 rows], then m and l [128]
 constexpr int kShortTiles = 8;        // caches of at most so many tiles are not cut
 constexpr int kMeta = 16;             // entries of the ring of group-validity bits
 constexpr int kStage = kTile * kD * 2;
@@ -653,8 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       const bool fix = drafts && flags[1] != 0;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       // a cut unit at the head of the share is its first record, one at the tail its second
-      float* part = a.ws + ((static_cast<int64_t>(blockIdx.x) * 2 + (g.u.tile > 0 ? 0 : 1)) * kRows +
-                            r) * kRec;
+      float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (g.u.tile > 0 ? 0 : 1)) * kRec + r;
 #pragma unroll 1
       for (int b = 0; b < kD / 32; ++b) {
         uint32_t o[32];
@@ -694,15 +693,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(part + b * 32);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          for (int i = 0; i < 32; ++i) part[(b * 32 + i) * kRows] = __uint_as_float(x[i]);
         }
       }
       if (live && !whole) {
-        part[kD] = m;
-        part[kD + 1] = l;
+        part[kD * kRows] = m;
+        part[(kD + 1) * kRows] = l;
       }
       tc5::fence_before();
     }
@@ -718,9 +715,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   if (threadIdx.x == 0 && flags[0]) report(a.err, KVQ_DEVERR_TIMEOUT);
 }
 
-// Joins the records of a cut unit: one warp per row.
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeArgs a) {
-  const int lane = threadIdx.x & 31;
+// Joins the records of a cut unit.  A block takes kJoinCols channels of all rows: thread = (row,
+// slice of the records), so that every read is along the rows as the records were written.
+constexpr int kJoinCols = 8, kJoinSlices = 4;
+
+__global__ void __launch_bounds__(kRows * kJoinSlices)
+tree_join_kernel(const __grid_constant__ TreeArgs a) {
+  __shared__ float part_sm[kJoinSlices][kJoinCols + 2][kRows];
   int64_t tiles, units;
   layer_totals(a, false, tiles, units);
   if (blockIdx.x >= units * a.n_layers) return;
@@ -730,41 +731,55 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
   const int c0 = static_cast<int>(u.start / share);
   const int c1 = static_cast<int>((u.start + u.q.tiles - 1) / share);
   if (c0 == c1) return;   // finished by its CTA
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int r = threadIdx.x % kRows, slice = threadIdx.x / kRows, col = blockIdx.y * kJoinCols;
   const int ri = r / a.G, node = u.r * a.tpt + ri;
-  if (ri >= a.tpt || node >= u.q.n) return;
-  auto rec = [&](int c) {   // the unit's start lies in c0's share, so there it is the tail
-    return a.ws + ((static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRows + r) * kRec;
-  };
-  float M = kNegInf;
-  for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, rec(c)[kD]);
+  const bool live = ri < a.tpt && node < u.q.n;
+  float M = kNegInf, l = 0.f, O[kJoinCols];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-  float O[8], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) O[e] = 0.f;
+  for (int e = 0; e < kJoinCols; ++e) O[e] = 0.f;
+  if (live) {
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float* p = rec(c);
-    const float mi = p[kD], f = mi == kNegInf ? 0.f : ex2_fast(mi - M);
-    l = fmaf(p[kD + 1], f, l);
+    for (int c = c0 + slice; c <= c1; c += kJoinSlices) {
+      // the unit's start lies in c0's share, so its record is the tail one there
+      const float* p = a.ws + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRec + r;
+      const float mi = p[kD * kRows], li = p[(kD + 1) * kRows];
+      float o[kJoinCols];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float4 o = *reinterpret_cast<const float4*>(p + e * 128 + lane * 4);
-      O[4 * e] = fmaf(o.x, f, O[4 * e]);
-      O[4 * e + 1] = fmaf(o.y, f, O[4 * e + 1]);
-      O[4 * e + 2] = fmaf(o.z, f, O[4 * e + 2]);
-      O[4 * e + 3] = fmaf(o.w, f, O[4 * e + 3]);
+      for (int e = 0; e < kJoinCols; ++e) o[e] = p[(col + e) * kRows];
+      const float Mn = fmaxf(M, mi);
+      const float f = M == kNegInf ? 0.f : ex2_fast(M - Mn), fi = mi == kNegInf ? 0.f : ex2_fast(mi - Mn);
+      l = l * f + li * fi;
+#pragma unroll
+      for (int e = 0; e < kJoinCols; ++e) O[e] = O[e] * f + o[e] * fi;
+      M = Mn;
     }
+  }
+#pragma unroll
+  for (int e = 0; e < kJoinCols; ++e) part_sm[slice][e][r] = O[e];
+  part_sm[slice][kJoinCols][r] = M;
+  part_sm[slice][kJoinCols + 1][r] = l;
+  __syncthreads();
+  if (slice > 0 || !live) return;
+  float Mx = M;
+#pragma unroll
+  for (int i = 1; i < kJoinSlices; ++i) Mx = fmaxf(Mx, part_sm[i][kJoinCols][r]);
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kJoinCols; ++e) O[e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kJoinSlices; ++i) {
+    const float mi = part_sm[i][kJoinCols][r], f = mi == kNegInf ? 0.f : ex2_fast(mi - Mx);
+    l = fmaf(part_sm[i][kJoinCols + 1][r], f, l);
+#pragma unroll
+    for (int e = 0; e < kJoinCols; ++e) O[e] = fmaf(part_sm[i][e][r], f, O[e]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t row = (static_cast<int64_t>(u.l) * a.total + u.q.n0 + node) * a.Hq + u.h * a.G +
                       (r - ri * a.G);
+  uint32_t y[kJoinCols / 2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
-    *reinterpret_cast<uint2*>(a.out + row * kD + e * 128 + lane * 4) =
-        make_uint2(pack_h2(O[4 * e] * inv, O[4 * e + 1] * inv),
-                   pack_h2(O[4 * e + 2] * inv, O[4 * e + 3] * inv));
+  for (int e = 0; e < kJoinCols; e += 2) y[e / 2] = pack_h2(O[e] * inv, O[e + 1] * inv);
+  *reinterpret_cast<uint4*>(a.out + row * kD + col) = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 // How a call is cut; the units are an upper bound (the lengths are on the device).
@@ -797,8 +812,8 @@ cudaError_t launch(const TreeArgs& a, const Plan& p, cudaStream_t cs) {
   tree_attn_kernel<BITS><<<p.grid, kThreads, Lay<BITS>::kTotal, cs>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole) return e;
-  const int rows = a.G * (a.max_nodes < p.tpt ? a.max_nodes : p.tpt);
-  tree_join_kernel<<<dim3(static_cast<unsigned>(p.units), (rows + 7) / 8), 256, 0, cs>>>(a);
+  tree_join_kernel<<<dim3(static_cast<unsigned>(p.units), kD / kJoinCols), kRows * kJoinSlices, 0,
+                     cs>>>(a);
   return cudaGetLastError();
 }
 
@@ -817,7 +832,7 @@ extern "C" size_t kvq_tree_attn_workspace(int n_layers, int nseq, int total_node
   const kvq::Plan p = kvq::plan_for(n_layers, nseq, total_nodes, num_kv_heads, num_q_heads,
                                     max_nodes, max_seq_len);
   if (p.whole) return 16;
-  return static_cast<size_t>(p.grid) * 2 * kvq::kRows * kvq::kRec * sizeof(float);
+  return static_cast<size_t>(p.grid) * 2 * kvq::kRec * sizeof(float);
 }
 
 extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_pools, int n_layers,
