@@ -233,7 +233,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     mbar_init(qfull, 1);
     mbar_init(odone, 1);
     mbar_init(odone + 1, 1);
-    for (int i = 0; i < NS; ++i) { mbar_init(sfull + i, 1); mbar_init(pready + i, kSoftmaxThreads); }
+    for (int i = 0; i < NS; ++i) { mbar_init(sfull + i, 1); mbar_init(pready + i, kSoftmaxThreads / 32); }
     tc5::fence_barrier_init();
     flags[0] = 0;
     flags[1] = 0;
@@ -301,7 +301,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     }
   } else if (warp == 4) {
     // ------------------------------------------------------------------- products (one thread)
-    if (lane == 0 && nt > 0) {
+    if (nt > 0 && tc5::elect_one()) {
       const uint32_t base = smem_u32(sm), ring = base + L::kRing;
       const uint64_t dk = tc5::desc_base(16), dv = tc5::desc_base(C::VR * 128);
       constexpr uint32_t id_s = tc5::idesc(BF, NB, false), id_o = tc5::idesc(BF, D, true);
@@ -452,7 +452,8 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         tc5::fence_smem();
       }
       tc5::fence_before();
-      mbar_arrive(pready + j % NS);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pready + j % NS);   // one per warp: arrivals of lanes queue up
     }
     if (ok && nt > 0) ok = warp_wait(odone + ((nt - 1) & 1), (nt - 1) >> 1 & 1, flags);
     if (!ok) flags[0] = 1;

@@ -42,7 +42,7 @@ namespace {
 constexpr int kD = 256;
 constexpr int kRows = 128;
 constexpr int kTile = 64;             // tokens per tile
-constexpr int kSoftmaxThreads = 128;  // warps 0-3
+constexpr int kSoftmaxWarps = 4;      // warps 0-3; one arrival per warp: arrivals of lanes queue up
 constexpr int kMmaWarp = 4, kCopyWarp = 5, kUnpackWarp0 = 6, kUnpackWarps = 8;
 constexpr int kThreads = (kUnpackWarp0 + kUnpackWarps) * 32;
 constexpr int kRec = (kD + 2) * kRows;   // a partial record: O [256][128 rows], then m and l [128]
@@ -244,12 +244,14 @@ __device__ __forceinline__ bool next_segment(const TreeArgs& a, Walk& w, Segment
   return g.u.s >= 0;
 }
 
-// 16 codes of a row (2 * BITS bytes at `src`, shared memory) times its scale, as two 16-byte
-// pieces in the stored order of channels.
-template <int BITS>
-__device__ __forceinline__ void unpack16(const unsigned char* src, uint32_t scale2, uint32_t o[8]) {
-  if constexpr (BITS == 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src);
+// 16 codes of a row (2 * BITS bytes in shared memory), and their product with the row's scale as
+// two 16-byte pieces in the stored order of channels.
+template <int BITS> struct Codes;
+
+template <> struct Codes<8> {
+  uint4 v;
+  __device__ __forceinline__ void load(const unsigned char* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void unpack(uint32_t scale2, uint32_t o[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -257,9 +259,18 @@ __device__ __forceinline__ void unpack16(const unsigned char* src, uint32_t scal
       o[2 * i] = hmul2u(hfma2u(prmt(u, 0x64646464u, 0x4140), kH1, kHm1152), scale2);
       o[2 * i + 1] = hmul2u(hfma2u(prmt(u, 0x64646464u, 0x4342), kH1, kHm1152), scale2);
     }
-  } else if constexpr (BITS == 6) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(src);
-    const uint32_t w0 = p[0], w1 = p[1], w2 = p[2];
+  }
+};
+
+template <> struct Codes<6> {
+  uint32_t w0, w1, w2;
+  __device__ __forceinline__ void load(const unsigned char* p) {
+    const uint32_t* x = reinterpret_cast<const uint32_t*>(p);
+    w0 = x[0];
+    w1 = x[1];
+    w2 = x[2];
+  }
+  __device__ __forceinline__ void unpack(uint32_t scale2, uint32_t o[8]) const {
     // per group of 4: low half bytes 0-1 (u0 at bit 0, u1 at 6), high half bytes 1-2 (u2 at 4,
     // u3 at 10): the mask leaves (u0, 16 u2), and after a shift by 6 (u1, 16 u3)
     const uint32_t x[4] = {prmt(w0, w0, 0x2110), prmt(w0, w1, 0x5443), prmt(w1, w2, 0x4332),
@@ -271,8 +282,13 @@ __device__ __forceinline__ void unpack16(const unsigned char* src, uint32_t scal
       o[2 * i] = hmul2u(hfma2u(a, 0x2C003C00u, 0xD600E420u), scale2);
       o[2 * i + 1] = hmul2u(hfma2u(b, 0x2C003C00u, 0xD600E420u), scale2);
     }
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(src);
+  }
+};
+
+template <> struct Codes<4> {
+  uint2 v;
+  __device__ __forceinline__ void load(const unsigned char* p) { v = *reinterpret_cast<const uint2*>(p); }
+  __device__ __forceinline__ void unpack(uint32_t scale2, uint32_t o[8]) const {
     const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -283,7 +299,7 @@ __device__ __forceinline__ void unpack16(const unsigned char* src, uint32_t scal
       o[4 * i + 3] = hmul2u(hfma2u((y & 0x00F000F0u) | 0x64006400u, kH16th, kHm72), scale2);
     }
   }
-}
+};
 
 // v_hat of channel d of a packed row in global memory (the rare path of non-finite drafts).
 template <int BITS>
@@ -330,15 +346,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) { mbar_init(rawfull + i, 1); mbar_init(rawempty + i, kUnpackWarps); }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(kfull + i, kUnpackWarps);
+      mbar_init(kfull + i, kUnpackWarps / 2);
       mbar_init(kempty + i, 1);
-      mbar_init(vfull + i, kUnpackWarps);
+      mbar_init(vfull + i, kUnpackWarps / 2);
       mbar_init(vempty + i, 1);
       mbar_init(sfull + i, 1);
-      mbar_init(pready + i, kSoftmaxThreads);
+      mbar_init(pready + i, kSoftmaxWarps);
       mbar_init(odone + i, 1);
     }
-    mbar_init(qready, kSoftmaxThreads);
+    mbar_init(qready, kSoftmaxWarps);
     mbar_init(drain, 1);
     tc5::fence_barrier_init();
     flags[0] = 0;
@@ -354,45 +370,79 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   bool ok = true;
 
   if (warp == kCopyWarp) {
-    // ------------------------------------------------------------------------- bulk copies
-    // Lane i looks up the page of 16-token group i of the next 8 tiles; then lanes 0-3 bring in
-    // each tile's four groups.
+    // ------------------------------------------------------------------------- copies
+    // Eight tiles at a time: lane i looks up the page of 16-token group i, then all lanes read
+    // those tiles' scales (lane = K or V, four tokens; scales of tokens that are not there become
+    // 0, so that their rows unpack to zeros).  The next eight are looked up while the tiles of
+    // the present ones go out, one bulk copy per group for each of K and V codes.
+    const int kind = lane >> 4, sub = lane & 15;
     while (ok && next_segment(a, w, g)) {
       const TreePools& P = a.L[g.u.l];
       const int total = g.u.q.len + g.u.q.n;
-      for (int b = 0; ok && b < g.count; b += 8) {
+      const uint16_t* scales = kind ? P.vs : P.ks;
+      auto page_of = [&](int b) {   // group `lane` of the tiles b .. b + 7 of the segment
         const int tg = (g.u.tile + b) * kTile + lane * 16;
-        int64_t row = -1;
-        if (b * 4 + lane < g.count * 4 && tg < total) {
-          const int lp = tg / a.ps;
-          const int page = lp < a.max_pages
-                               ? __ldg(a.pt + static_cast<int64_t>(g.u.s) * a.max_pages + lp) : -1;
-          if (page >= 0 && page < P.k_pages && page < P.v_pages)
-            row = (static_cast<int64_t>(page) * a.H + g.u.h) * a.ps + (tg - lp * a.ps);
-          else
-            report(a.err, KVQ_DEVERR_PAGE_RANGE);
+        if (b + (lane >> 2) >= g.count || tg >= total) return -2;
+        const int lp = tg / a.ps;
+        return lp < a.max_pages ? __ldg(a.pt + static_cast<int64_t>(g.u.s) * a.max_pages + lp) : -1;
+      };
+      auto row_of = [&](int b, int page) -> int64_t {
+        if (page == -2) return -1;
+        if (page < 0 || page >= P.k_pages || page >= P.v_pages) {
+          report(a.err, KVQ_DEVERR_PAGE_RANGE);
+          return -1;
         }
-        for (int j = 0; j < 8 && b + j < g.count; ++j, ++it) {
-          const int64_t r = __shfl_sync(kFullMask, row, j * 4 + (lane & 3));
+        const int tg = (g.u.tile + b) * kTile + lane * 16;
+        return (static_cast<int64_t>(page) * a.H + g.u.h) * a.ps + tg % a.ps;
+      };
+      auto load_scales = [&](int64_t rows, uint2 x[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t r = __shfl_sync(kFullMask, rows, j * 4 + (sub >> 2));
+          x[j] = r >= 0 ? ld_nc_v2(scales + r + (sub & 3) * 4) : make_uint2(0, 0);
+        }
+      };
+      int64_t rows = row_of(0, page_of(0)), next_rows = -1;
+      int page = -2;
+      uint2 x[8], nx[8];
+      load_scales(rows, x);
+      for (int b = 0; ok && b < g.count; b += 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j == 0) page = page_of(b + 8);
+          if (j == 4) {
+            next_rows = row_of(b + 8, page);
+            load_scales(next_rows, nx);
+          }
+          if (!ok || b + j >= g.count) continue;
           const int st = it % R;
           if (it >= R) ok = warp_wait(rawempty + st, (it / R + 1) & 1, flags);
-          if (!ok) break;
+          if (!ok) continue;
+          unsigned char* dst = sm + L::kRawAt + st * L::kRaw;
+          const int left = total - ((g.u.tile + b + j) * kTile + sub * 4);   // tokens still there
+          if (left < 4) {
+            if (left < 1) x[j].x &= 0xffff0000u;
+            if (left < 2) x[j].x &= 0x0000ffffu;
+            if (left < 3) x[j].y &= 0xffff0000u;
+            x[j].y &= 0x0000ffffu;
+          }
+          *reinterpret_cast<uint2*>(dst + 2 * kTile * L::kPd + kind * 2 * kTile + sub * 8) = x[j];
+          const int64_t r = __shfl_sync(kFullMask, rows, j * 4 + (lane & 3));
           const unsigned have = __ballot_sync(kFullMask, lane < 4 && r >= 0);
           if (lane == 0) {
             meta[it % kMeta] = static_cast<int>(have);
-            mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd + 64));
+            mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd));
           }
           __syncwarp();
-          if (lane < 4 && r >= 0) {
-            unsigned char* dst = sm + L::kRawAt + st * L::kRaw;
-            bulk_g2s(dst + lane * 16 * L::kPd, P.kc + r * L::kPd, 16 * L::kPd, rawfull + st);
-            bulk_g2s(dst + (kTile + lane * 16) * L::kPd, P.vc + r * L::kPd, 16 * L::kPd,
-                     rawfull + st);
-            bulk_g2s(dst + 2 * kTile * L::kPd + lane * 32, P.ks + r, 32, rawfull + st);
-            bulk_g2s(dst + 2 * kTile * L::kPd + 2 * kTile + lane * 32, P.vs + r, 32, rawfull + st);
-          }
+          if (lane < 8 && r >= 0)   // lanes 0-3 the keys' groups, 4-7 the values'
+            bulk_g2s(dst + ((lane >> 2) * kTile + (lane & 3) * 16) * L::kPd,
+                     (lane < 4 ? P.kc : P.vc) + r * L::kPd, 16 * L::kPd, rawfull + st);
           __syncwarp();
+          ++it;
         }
+        rows = next_rows;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = nx[j];
       }
     }
     if (!ok) {   // wait for the copies in flight
@@ -405,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     constexpr uint32_t id_s = tc5::idesc(false, kTile, false), id_o = tc5::idesc(false, kD, true);
     int seg = 0;
     while (ok && next_segment(a, w, g)) {
-      if (lane == 0) {
+      if (tc5::elect_one()) {
         auto product_s = [&](int i) {
           ok = ok && tc5::wait(kfull + (i & 1), (i >> 1) & 1, flags);
           if (!ok) return;
@@ -441,73 +491,82 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           if (ok) product_o(it + j, j == 0);
         }
       }
-      ok = __shfl_sync(kFullMask, ok, 0);
+      ok = __all_sync(kFullMask, ok);
       it += g.count;
       ++seg;
     }
     if (!ok) {   // what was issued must end before the memory is given back
       flags[0] = 1;
-      if (lane == 0) {
+      if (tc5::elect_one()) {
         tc5::commit(drain);
         mbar_wait_bounded(drain, 0);
       }
     }
   } else if (warp >= kUnpackWarp0) {
     // ------------------------------------------------------------------------------- unpack
-    // A warp's step takes two rows: lanes 8q .. 8q+7 hold panel q (64 channels) of both, four
-    // 16-channel units each, which spreads a quarter-warp's 16-byte stores over all banks.
+    // Four warps for K and four for V, so that neither waits for the other's products.  A warp's
+    // step takes two rows: lanes 8q .. 8q+7 hold panel q (64 channels) of both, four 16-channel
+    // units each, which spreads a quarter-warp's 16-byte stores over all banks.  A tile's codes
+    // are all read before the first is stored: reads and stores would otherwise alternate, each
+    // waiting for the other.
+    const int kv = (warp - kUnpackWarp0) >> 2, uw = (warp - kUnpackWarp0) & 3;
     const int q = lane >> 3, rr = (lane >> 2) & 1, u = lane & 3;
     const int src = (q * 4 + u) * 2 * BITS;
+    uint64_t *full = kv ? vfull : kfull, *empty = kv ? vempty : kempty;
+    unsigned char* stages = sm + (kv ? L::kV : L::kK) + q * kTile * 128;
+    constexpr int S = kTile / 8;   // steps: 16 rows per warp
     while (ok && next_segment(a, w, g)) {
-      const int len = g.u.q.len, total = len + g.u.q.n;
+      const int len = g.u.q.len;
       for (int j = 0; j < g.count; ++j, ++it) {
         const int st = it % R, t0 = (g.u.tile + j) * kTile;
         ok = warp_wait(rawfull + st, (it / R) & 1, flags);
         if (!ok) break;
-        const unsigned have = static_cast<unsigned>(meta[it % kMeta]);
-        const unsigned char* raw = sm + L::kRawAt + st * L::kRaw;
-        const uint16_t* sc = reinterpret_cast<const uint16_t*>(raw + 2 * kTile * L::kPd);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          uint64_t* empty = (kv ? vempty : kempty) + (it & 1);
-          if (it >= 2) ok = warp_wait(empty, (it / 2 + 1) & 1, flags);
-          if (!ok) break;
-          unsigned char* dst = sm + (kv ? L::kV : L::kK) + (it & 1) * kStage + q * kTile * 128;
-          bool found = false;
+        const unsigned char* raw = sm + L::kRawAt + st * L::kRaw + kv * kTile * L::kPd;
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(
+            sm + L::kRawAt + st * L::kRaw + 2 * kTile * L::kPd + kv * 2 * kTile);
+        Codes<BITS> c[S];
+        uint32_t s1[S];
 #pragma unroll
-          for (int i = 0; i < kTile / 2 / kUnpackWarps; ++i) {
-            const int row = (i * kUnpackWarps + warp - kUnpackWarp0) * 2 + rr;
-            // rows that are not there become zeros (a code is always finite)
-            const bool there = t0 + row < total && (have >> (row >> 4) & 1);
-            const uint32_t s1 = there ? sc[kv * kTile + row] : 0u;
-            uint32_t o[8];
-            unpack16<BITS>(raw + (kv * kTile + row) * L::kPd + src, s1 | (s1 << 16), o);
-            if (kv && t0 + kTile > len && t0 + row >= len) {
-              // a draft only some rows see: 0 * inf must not reach the others
-              bool bad = false;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) bad = bad || nonfinite2(o[e]);
-              if (bad) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  if ((o[e] & 0x7c00u) == 0x7c00u) o[e] &= 0xffff0000u;
-                  if ((o[e] & 0x7c000000u) == 0x7c000000u) o[e] &= 0x0000ffffu;
-                }
-                found = true;
-              }
-            }
-            unsigned char* p = dst + row * 128;
-            const int at = ((2 * u) ^ (row & 7)) * 16;
-            *reinterpret_cast<uint4*>(p + at) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(p + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          if (found) flags[1] = 1;
-          tc5::fence_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive((kv ? vfull : kfull) + (it & 1));
+        for (int i = 0; i < S; ++i) {
+          const int row = (i * 4 + uw) * 2 + rr;
+          c[i].load(raw + row * L::kPd + src);
+          s1[i] = sc[row];
         }
+        if (it >= 2) ok = warp_wait(empty + (it & 1), (it / 2 + 1) & 1, flags);
         if (!ok) break;
-        if (lane == 0) mbar_arrive(rawempty + st);
+        unsigned char* dst = stages + (it & 1) * kStage;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const int row = (i * 4 + uw) * 2 + rr;
+          uint32_t o[8];
+          c[i].unpack(s1[i] | (s1[i] << 16), o);
+          if (kv && t0 + kTile > len && t0 + row >= len) {
+            // a draft only some rows see: 0 * inf must not reach the others
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) bad = bad || nonfinite2(o[e]);
+            if (bad) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if ((o[e] & 0x7c00u) == 0x7c00u) o[e] &= 0xffff0000u;
+                if ((o[e] & 0x7c000000u) == 0x7c000000u) o[e] &= 0x0000ffffu;
+              }
+              found = true;
+            }
+          }
+          unsigned char* p = dst + row * 128;
+          const int at = ((2 * u) ^ (row & 7)) * 16;
+          *reinterpret_cast<uint4*>(p + at) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(p + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        if (found) flags[1] = 1;
+        tc5::fence_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full + (it & 1));
+          mbar_arrive(rawempty + st);
+        }
       }
     }
   } else {
@@ -546,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       }
       tc5::wait_st();
       tc5::fence_before();
-      mbar_arrive(qready);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
       // the ancestors, if drafts are among this segment's tokens
       uint64_t seen = 0;
       const bool drafts = (g.u.tile + g.count) * kTile > q.len;
@@ -643,7 +703,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         l += (l0 + l1) + (l2 + l3);
         tc5::wait_st();
         tc5::fence_before();
-        mbar_arrive(pready + (it & 1));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pready + (it & 1));
       }
       if (!ok) break;
       ok = warp_wait(odone + ((it - 1) & 1), (it - 1) >> 1 & 1, flags);
