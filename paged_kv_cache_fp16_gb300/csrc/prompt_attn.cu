@@ -246,7 +246,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
 
   if (warp == 5) {
     // ---------------------------------------------------------------- tensor copies (one thread)
-    if (lane == 0 && nt > 0) {
+    if (nt > 0 && tc5::elect_one()) {
       mbar_expect_tx(qfull, (D / 64) * 128 * a.tpt * a.G);
       for (int p = 0; p < D / 64; ++p)
         tc5::tma_load_3d(sm + p * kRows * 128, &mq, p * 64, n.h * a.G, n.q0 + i0, qfull);

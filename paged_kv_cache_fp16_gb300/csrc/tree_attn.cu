@@ -45,7 +45,7 @@ constexpr int kTile = 64;             // tokens per tile
 constexpr int kSoftmaxWarps = 4;      // warps 0-3; one arrival per warp: arrivals of lanes queue up
 constexpr int kMmaWarp = 4, kCopyWarp = 5, kUnpackWarp0 = 6, kUnpackWarps = 8;
 constexpr int kThreads = (kUnpackWarp0 + kUnpackWarps) * 32;
-constexpr int kRec = (kD + 2) * kRows;   // a partial record: O [256][128 rows], then m and l [128]
+constexpr int kRec = (kD + 2) * kRows;   // a partial record: O [256 / 4][128 rows][4], then m and l [128]
 constexpr int kShortTiles = 8;        // caches of at most so many tiles are not cut
 constexpr int kMeta = 16;             // entries of the ring of group-validity bits
 constexpr int kStage = kTile * kD * 2;
@@ -119,60 +119,55 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int s, bool check) {
   return q;
 }
 
-__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+__device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(kFullMask, x, o);
+    const uint32_t y = __shfl_up_sync(kFullMask, x, o);
     if (lane >= o) x += y;
   }
   return x;
 }
 
-// Tiles and units of one layer (whole warp).
-__device__ __forceinline__ void layer_totals(const TreeArgs& a, bool check, int64_t& tiles,
-                                             int64_t& units) {
+// Tiles and units of one layer (whole warp).  The call's tiles fit 31 bits.
+__device__ __forceinline__ void layer_totals(const TreeArgs& a, bool check, uint32_t& tiles,
+                                             uint32_t& units) {
   const int lane = threadIdx.x & 31;
-  int64_t t = 0, u = 0;
+  uint32_t t = 0, u = 0;
   for (int s = lane; s < a.nseq; s += 32) {
     const Seq q = seq_of(a, s, check);
-    u += static_cast<int64_t>(q.rt) * a.H;
-    t += static_cast<int64_t>(q.rt) * a.H * q.tiles;
+    u += static_cast<uint32_t>(q.rt) * a.H;
+    t += static_cast<uint32_t>(q.rt) * a.H * q.tiles;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    t += __shfl_xor_sync(kFullMask, t, o);
-    u += __shfl_xor_sync(kFullMask, u, o);
-  }
-  tiles = t;
-  units = u;
+  tiles = __reduce_add_sync(kFullMask, t);
+  units = __reduce_add_sync(kFullMask, u);
 }
 
 struct Unit {
   Seq q;
   int l, s, h, r;    // layer, sequence, KV head, row tile
   int tile;          // the tile sought
-  int64_t start;     // the unit's first tile in the line of all tiles
+  uint32_t start;    // the unit's first tile in the line of all tiles
 };
 
 // The unit that holds tile `at` of the line of all tiles (BY_TILE), or unit number `at`; whole
 // warp, `at` in range.
 template <bool BY_TILE>
-__device__ __forceinline__ Unit find_unit(const TreeArgs& a, int64_t at, int64_t layer_tiles,
-                                          int64_t layer_units) {
+__device__ __forceinline__ Unit find_unit(const TreeArgs& a, uint32_t at, uint32_t layer_tiles,
+                                          uint32_t layer_units) {
   const int lane = threadIdx.x & 31;
   Unit r;
-  const int64_t per = BY_TILE ? layer_tiles : layer_units;
-  r.l = static_cast<int>(at / per);
-  const int64_t x = at - r.l * per;
-  int64_t before = 0, tiles_before = 0;
+  const uint32_t per = BY_TILE ? layer_tiles : layer_units;
+  r.l = a.n_layers == 1 ? 0 : static_cast<int>(at / per);
+  const uint32_t x = at - r.l * per;
+  uint32_t before = 0, tiles_before = 0;
   for (int base = 0; base < a.nseq; base += 32) {
     const Seq q = seq_of(a, base + lane, false);
-    const int64_t units = static_cast<int64_t>(q.rt) * a.H, tiles = units * q.tiles;
-    const int64_t mine = BY_TILE ? tiles : units;
-    const int64_t incl = warp_scan(mine), tincl = BY_TILE ? incl : warp_scan(tiles);
-    const int64_t start = before + incl - mine;
-    const unsigned hit = __ballot_sync(kFullMask, x >= start && x < start + mine);
+    const uint32_t units = static_cast<uint32_t>(q.rt) * a.H, tiles = units * q.tiles;
+    const uint32_t mine = BY_TILE ? tiles : units;
+    const uint32_t incl = warp_scan(mine), tincl = BY_TILE ? incl : warp_scan(tiles);
+    const uint32_t start = before + incl - mine;
+    const unsigned hit = __ballot_sync(kFullMask, x >= start && x - start < mine);
     if (hit) {
       const int src = __ffs(hit) - 1;
       r.s = base + src;
@@ -181,12 +176,12 @@ __device__ __forceinline__ Unit find_unit(const TreeArgs& a, int64_t at, int64_t
       r.q.len = __shfl_sync(kFullMask, q.len, src);
       r.q.tiles = __shfl_sync(kFullMask, q.tiles, src);
       r.q.rt = __shfl_sync(kFullMask, q.rt, src);
-      const int64_t rem = x - __shfl_sync(kFullMask, start, src);
-      const int64_t tstart = tiles_before + __shfl_sync(kFullMask, tincl - tiles, src);
-      const int64_t u = BY_TILE ? rem / r.q.tiles : rem;
+      const uint32_t rem = x - __shfl_sync(kFullMask, start, src);
+      const uint32_t tstart = tiles_before + __shfl_sync(kFullMask, tincl - tiles, src);
+      const uint32_t u = BY_TILE ? rem / static_cast<uint32_t>(r.q.tiles) : rem;
       r.tile = BY_TILE ? static_cast<int>(rem - u * r.q.tiles) : 0;
-      r.h = static_cast<int>(u / r.q.rt);
-      r.r = static_cast<int>(u - static_cast<int64_t>(r.h) * r.q.rt);
+      r.h = static_cast<int>(u / static_cast<uint32_t>(r.q.rt));
+      r.r = static_cast<int>(u) - r.h * r.q.rt;
       r.start = r.l * layer_tiles + tstart + u * r.q.tiles;
       return r;
     }
@@ -199,13 +194,12 @@ __device__ __forceinline__ Unit find_unit(const TreeArgs& a, int64_t at, int64_t
 
 // A CTA's way through its share: segments (a unit's consecutive tiles).  Every role walks it.
 struct Walk {
-  int64_t at, end, step, layer_tiles, layer_units;
+  uint32_t at, end, layer_tiles, layer_units;
   bool whole;
 };
 
-__device__ __forceinline__ int64_t share_of(const TreeArgs& a, int64_t layer_tiles) {
-  const int64_t all = layer_tiles * a.n_layers;
-  return (all + a.grid - 1) / a.grid;
+__device__ __forceinline__ uint32_t share_of(const TreeArgs& a, uint32_t layer_tiles) {
+  return (layer_tiles * a.n_layers + a.grid - 1) / a.grid;
 }
 
 __device__ __forceinline__ Walk walk_of(const TreeArgs& a, bool check) {
@@ -215,12 +209,10 @@ __device__ __forceinline__ Walk walk_of(const TreeArgs& a, bool check) {
   if (w.whole) {
     w.at = blockIdx.x;
     w.end = w.layer_units * a.n_layers;
-    w.step = a.grid;
   } else {
-    const int64_t share = share_of(a, w.layer_tiles), all = w.layer_tiles * a.n_layers;
-    w.at = min(all, share * blockIdx.x);
+    const uint32_t share = share_of(a, w.layer_tiles), all = w.layer_tiles * a.n_layers;
+    w.at = min(all, share * blockIdx.x);   // share * grid < all + grid: no overflow
     w.end = min(all, w.at + share);
-    w.step = 0;
   }
   return w;
 }
@@ -235,10 +227,10 @@ __device__ __forceinline__ bool next_segment(const TreeArgs& a, Walk& w, Segment
   if (w.whole) {
     g.u = find_unit<false>(a, w.at, w.layer_tiles, w.layer_units);
     g.count = g.u.q.tiles;
-    w.at += w.step;
+    w.at += a.grid;
   } else {
     g.u = find_unit<true>(a, w.at, w.layer_tiles, w.layer_units);
-    g.count = static_cast<int>(min(static_cast<int64_t>(g.u.q.tiles - g.u.tile), w.end - w.at));
+    g.count = static_cast<int>(min(static_cast<uint32_t>(g.u.q.tiles - g.u.tile), w.end - w.at));
     w.at += g.count;
   }
   return g.u.s >= 0;
@@ -427,16 +419,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             x[j].y &= 0x0000ffffu;
           }
           *reinterpret_cast<uint2*>(dst + 2 * kTile * L::kPd + kind * 2 * kTile + sub * 8) = x[j];
-          const int64_t r = __shfl_sync(kFullMask, rows, j * 4 + (lane & 3));
-          const unsigned have = __ballot_sync(kFullMask, lane < 4 && r >= 0);
-          if (lane == 0) {
-            meta[it % kMeta] = static_cast<int>(have);
-            mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd));
+          int64_t r[4];
+          unsigned have = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            r[i] = __shfl_sync(kFullMask, rows, j * 4 + i);
+            have |= (r[i] >= 0 ? 1u : 0u) << i;
           }
           __syncwarp();
-          if (lane < 8 && r >= 0)   // lanes 0-3 the keys' groups, 4-7 the values'
-            bulk_g2s(dst + ((lane >> 2) * kTile + (lane & 3) * 16) * L::kPd,
-                     (lane < 4 ? P.kc : P.vc) + r * L::kPd, 16 * L::kPd, rawfull + st);
+          if (tc5::elect_one()) {   // copies by several lanes at once take 100 cycles each
+            meta[it % kMeta] = static_cast<int>(have);
+            mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (r[i] < 0) continue;
+              bulk_g2s(dst + i * 16 * L::kPd, P.kc + r[i] * L::kPd, 16 * L::kPd, rawfull + st);
+              bulk_g2s(dst + (kTile + i * 16) * L::kPd, P.vc + r[i] * L::kPd, 16 * L::kPd,
+                       rawfull + st);
+            }
+          }
           __syncwarp();
           ++it;
         }
@@ -535,30 +536,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (it >= 2) ok = warp_wait(empty + (it & 1), (it / 2 + 1) & 1, flags);
         if (!ok) break;
         unsigned char* dst = stages + (it & 1) * kStage;
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < S; ++i) {
-          const int row = (i * 4 + uw) * 2 + rr;
-          uint32_t o[8];
-          c[i].unpack(s1[i] | (s1[i] << 16), o);
-          if (kv && t0 + kTile > len && t0 + row >= len) {
-            // a draft only some rows see: 0 * inf must not reach the others
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) bad = bad || nonfinite2(o[e]);
-            if (bad) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if ((o[e] & 0x7c00u) == 0x7c00u) o[e] &= 0xffff0000u;
-                if ((o[e] & 0x7c000000u) == 0x7c000000u) o[e] &= 0x0000ffffu;
-              }
-              found = true;
-            }
-          }
+        auto store = [&](int row, const uint32_t o[8]) {
           unsigned char* p = dst + row * 128;
           const int at = ((2 * u) ^ (row & 7)) * 16;
           *reinterpret_cast<uint4*>(p + at) = make_uint4(o[0], o[1], o[2], o[3]);
           *reinterpret_cast<uint4*>(p + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+        };
+        bool found = false;
+        if (!(kv && t0 + kTile > len)) {   // no branch inside: the steps overlap
+#pragma unroll
+          for (int i = 0; i < S; ++i) {
+            uint32_t o[8];
+            c[i].unpack(s1[i] | (s1[i] << 16), o);
+            store((i * 4 + uw) * 2 + rr, o);
+          }
+        } else {   // drafts among the values: 0 * inf must not reach the rows that do not see them
+#pragma unroll
+          for (int i = 0; i < S; ++i) {
+            const int row = (i * 4 + uw) * 2 + rr;
+            uint32_t o[8];
+            c[i].unpack(s1[i] | (s1[i] << 16), o);
+            if (t0 + row >= len) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if (nonfinite2(o[e])) found = true;
+                if ((o[e] & 0x7c00u) == 0x7c00u) o[e] &= 0xffff0000u;
+                if ((o[e] & 0x7c000000u) == 0x7c000000u) o[e] &= 0x0000ffffu;
+              }
+            }
+            store(row, o);
+          }
         }
         if (found) flags[1] = 1;
         tc5::fence_smem();
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       const bool fix = drafts && flags[1] != 0;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       // a cut unit at the head of the share is its first record, one at the tail its second
-      float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (g.u.tile > 0 ? 0 : 1)) * kRec + r;
+      float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (g.u.tile > 0 ? 0 : 1)) * kRec;
 #pragma unroll 1
       for (int b = 0; b < kD / 32; ++b) {
         uint32_t o[32];
@@ -754,13 +761,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         } else {
+          uint4* dst = reinterpret_cast<uint4*>(part) + b * 8 * kRows + r;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) part[(b * 32 + i) * kRows] = __uint_as_float(x[i]);
+          for (int i = 0; i < 8; ++i)
+            dst[i * kRows] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         }
       }
       if (live && !whole) {
-        part[kD * kRows] = m;
-        part[(kD + 1) * kRows] = l;
+        part[kD * kRows + r] = m;
+        part[(kD + 1) * kRows + r] = l;
       }
       tc5::fence_before();
     }
@@ -783,12 +792,12 @@ constexpr int kJoinCols = 8, kJoinSlices = 4;
 __global__ void __launch_bounds__(kRows * kJoinSlices)
 tree_join_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ float part_sm[kJoinSlices][kJoinCols + 2][kRows];
-  int64_t tiles, units;
+  uint32_t tiles, units;
   layer_totals(a, false, tiles, units);
   if (blockIdx.x >= units * a.n_layers) return;
   const Unit u = find_unit<false>(a, blockIdx.x, tiles, units);
   if (u.s < 0) return;
-  const int64_t share = share_of(a, tiles);
+  const uint32_t share = share_of(a, tiles);
   const int c0 = static_cast<int>(u.start / share);
   const int c1 = static_cast<int>((u.start + u.q.tiles - 1) / share);
   if (c0 == c1) return;   // finished by its CTA
@@ -802,11 +811,13 @@ tree_join_kernel(const __grid_constant__ TreeArgs a) {
 #pragma unroll 4
     for (int c = c0 + slice; c <= c1; c += kJoinSlices) {
       // the unit's start lies in c0's share, so its record is the tail one there
-      const float* p = a.ws + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRec + r;
-      const float mi = p[kD * kRows], li = p[(kD + 1) * kRows];
-      float o[kJoinCols];
+      const float* p = a.ws + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRec;
+      const float mi = p[kD * kRows + r], li = p[(kD + 1) * kRows + r];
+      float4 o4[kJoinCols / 4];
 #pragma unroll
-      for (int e = 0; e < kJoinCols; ++e) o[e] = p[(col + e) * kRows];
+      for (int e = 0; e < kJoinCols / 4; ++e)
+        o4[e] = reinterpret_cast<const float4*>(p)[(col / 4 + e) * kRows + r];
+      const float* o = reinterpret_cast<const float*>(o4);
       const float Mn = fmaxf(M, mi);
       const float f = M == kNegInf ? 0.f : ex2_fast(M - Mn), fi = mi == kNegInf ? 0.f : ex2_fast(mi - Mn);
       l = l * f + li * fi;
@@ -943,9 +954,11 @@ extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_p
   if (workspace_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
   const Plan p = plan_for(n_layers, nseq, total_nodes, H, num_q_heads, max_nodes, max_seq_len);
-  if (p.units > INT32_MAX)
-    return fail(KVQ_ERR_RANGE, "%s: %lld row tiles exceed the grid", fn,
-                static_cast<long long>(p.units));
+  const int64_t seq_tiles = (static_cast<int64_t>(max_seq_len) + kTile - 1) / kTile;
+  if (p.units > INT32_MAX / 2 || p.units * (seq_tiles < 1 ? 1 : seq_tiles) > INT32_MAX / 2)
+    return fail(KVQ_ERR_RANGE, "%s: %lld units (layers x KV heads x tiles of 128 rows) of up to "
+                "%lld tiles of 64 tokens exceed 2^30 tiles", fn, static_cast<long long>(p.units),
+                static_cast<long long>(seq_tiles));
   TreeArgs a;
   for (int i = 0; i < KVQ_MAX_TENSORS; ++i)
     a.L[i] = i < n_layers ? TreePools{k_pools[i].codes, k_pools[i].scales, v_pools[i].codes,
