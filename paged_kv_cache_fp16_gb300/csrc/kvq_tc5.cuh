@@ -173,5 +173,84 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
 constexpr float kOff = 10.f;
 constexpr float kSlack = 4.f;
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The largest of N scores (float32 patterns); NaN only if all are.
+template <int N>
+__device__ __forceinline__ float row_max(const uint32_t s[N]) {
+  const float ninf = __uint_as_float(0xff800000u);
+  float m[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      m[j] = max3(m[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// 16-bit pairs of float32 values, rounded to nearest even.
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The weights 2^(s c - mo) of N scores, rounded to 16 bits, to the TMEM columns from `to` on;
+// returns their float32 sum.  Two elements per multiply-add and per addition (packed float32).
+template <bool BF, int N>
+__device__ __forceinline__ float weights(const uint32_t s[N], float c, float mo, uint32_t to) {
+  const uint64_t c2 = pair(__float_as_uint(c), __float_as_uint(c));
+  const uint64_t m2 = pair(__float_as_uint(-mo), __float_as_uint(-mo));
+  uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+  for (int b = 0; b < N / 32; ++b) {
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+      float x0, x1, x2, x3;
+      unpair(fma2(pair(s[b * 32 + i], s[b * 32 + i + 1]), c2, m2), x0, x1);
+      unpair(fma2(pair(s[b * 32 + i + 2], s[b * 32 + i + 3]), c2, m2), x2, x3);
+      x0 = ex2_fast(x0);
+      x1 = ex2_fast(x1);
+      x2 = ex2_fast(x2);
+      x3 = ex2_fast(x3);
+      sum0 = add2(sum0, pair(__float_as_uint(x0), __float_as_uint(x1)));
+      sum1 = add2(sum1, pair(__float_as_uint(x2), __float_as_uint(x3)));
+      p[i / 2] = pack2<BF>(x0, x1);
+      p[i / 2 + 1] = pack2<BF>(x2, x3);
+    }
+    st16(to + b * 16, p);
+  }
+  float a, b;
+  unpair(add2(sum0, sum1), a, b);
+  return a + b;
+}
+
 }  // namespace tc5
 }  // namespace kvq

@@ -144,14 +144,6 @@ __device__ __forceinline__ int keys_seen(const Unit& n, int i) {
   return max(0, min(n.lk, i + n.lk - n.lq + 1));
 }
 
-template <bool BF> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  if constexpr (BF) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&b);
-  } else {
-    return pack_h2(lo, hi);
-  }
-}
 template <bool BF> __device__ __forceinline__ float to_f(uint16_t b) {
   if constexpr (BF) return __uint_as_float(static_cast<uint32_t>(b) << 16);
   else return h2f(b);
@@ -385,15 +377,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         for (int i = 0; i < NB; ++i)
           if (t0 + i >= limit) s[i] = 0xff800000u;
       }
-      float mx0 = kNegInf, mx1 = kNegInf, mx2 = kNegInf, mx3 = kNegInf;
-#pragma unroll
-      for (int i = 0; i < NB; i += 4) {
-        mx0 = fmaxf(mx0, __uint_as_float(s[i]));
-        mx1 = fmaxf(mx1, __uint_as_float(s[i + 1]));
-        mx2 = fmaxf(mx2, __uint_as_float(s[i + 2]));
-        mx3 = fmaxf(mx3, __uint_as_float(s[i + 3]));
-      }
-      const float x = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.c;
+      const float x = tc5::row_max<NB>(s) * a.c;
       if (j == 0) {
         m = x;
       } else {
@@ -418,23 +402,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         }
       }
       const float mo = m == kNegInf ? 0.f : m - tc5::kOff;
-      float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-      for (int q = 0; q < NB / 32; ++q) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float p0 = ex2_fast(fmaf(__uint_as_float(s[q * 32 + i]), a.c, -mo));
-          const float p1 = ex2_fast(fmaf(__uint_as_float(s[q * 32 + i + 1]), a.c, -mo));
-          const float p2 = ex2_fast(fmaf(__uint_as_float(s[q * 32 + i + 2]), a.c, -mo));
-          const float p3 = ex2_fast(fmaf(__uint_as_float(s[q * 32 + i + 3]), a.c, -mo));
-          l0 += p0; l1 += p1; l2 += p2; l3 += p3;
-          p[i / 2] = pack2<BF>(p0, p1);
-          p[i / 2 + 1] = pack2<BF>(p2, p3);
-        }
-        tc5::st16(sb + q * 16, p);
-      }
-      l += (l0 + l1) + (l2 + l3);
+      l += tc5::weights<BF, NB>(s, a.c, mo, sb);
       tc5::wait_st();
       if (edge) {
         // a slot's phase is told by its parity: the load before the one waited for must be known
@@ -497,7 +465,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            w[e] = pack2<BF>(__uint_as_float(o[i * 8 + e * 2]), __uint_as_float(o[i * 8 + e * 2 + 1]));
+            w[e] = tc5::pack2<BF>(__uint_as_float(o[i * 8 + e * 2]), __uint_as_float(o[i * 8 + e * 2 + 1]));
           dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       } else {
@@ -568,7 +536,7 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant_
 #pragma unroll
   for (int e = 0; e < E; e += 2)
     *reinterpret_cast<uint32_t*>(a.out + row * D + e * 32 + lane * 2) =
-        pack2<BF>(O[e] * inv, O[e + 1] * inv);
+        tc5::pack2<BF>(O[e] * inv, O[e + 1] * inv);
   if (a.lse && lane == 0)
     a.lse[row] = M == kNegInf ? kNegInf : (M - tc5::kOff + log2f(l)) * 0.6931471805599453f;
 }

@@ -47,6 +47,7 @@ constexpr int kMmaWarp = 4, kCopyWarp = 5, kUnpackWarp0 = 6, kUnpackWarps = 8;
 constexpr int kThreads = (kUnpackWarp0 + kUnpackWarps) * 32;
 constexpr int kRec = (kD + 2) * kRows;   // a partial record: O [256 / 4][128 rows][4], then m and l [128]
 constexpr int kShortTiles = 8;        // caches of at most so many tiles are not cut
+constexpr uint32_t kNoRow = 0xffffffffu;
 constexpr int kMeta = 16;             // entries of the ring of group-validity bits
 constexpr int kStage = kTile * kD * 2;
 constexpr uint32_t kColS = 256, kColQ = 384, kCols = 512;   // TMEM: O at 0, S at 256 and 320, Q
@@ -378,23 +379,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         const int lp = tg / a.ps;
         return lp < a.max_pages ? __ldg(a.pt + static_cast<int64_t>(g.u.s) * a.max_pages + lp) : -1;
       };
-      auto row_of = [&](int b, int page) -> int64_t {
-        if (page == -2) return -1;
+      // Row numbers fit 32 bits: 2^32 - 1 rows of 128 bytes are more than the device's memory.
+      auto row_of = [&](int b, int page) -> uint32_t {
+        if (page == -2) return kNoRow;
         if (page < 0 || page >= P.k_pages || page >= P.v_pages) {
           report(a.err, KVQ_DEVERR_PAGE_RANGE);
-          return -1;
+          return kNoRow;
         }
         const int tg = (g.u.tile + b) * kTile + lane * 16;
-        return (static_cast<int64_t>(page) * a.H + g.u.h) * a.ps + tg % a.ps;
+        return (static_cast<uint32_t>(page) * a.H + g.u.h) * a.ps + tg % a.ps;
       };
-      auto load_scales = [&](int64_t rows, uint2 x[8]) {
+      auto load_scales = [&](uint32_t rows, uint2 x[8]) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int64_t r = __shfl_sync(kFullMask, rows, j * 4 + (sub >> 2));
-          x[j] = r >= 0 ? ld_nc_v2(scales + r + (sub & 3) * 4) : make_uint2(0, 0);
+          const uint32_t r = __shfl_sync(kFullMask, rows, j * 4 + (sub >> 2));
+          x[j] = r != kNoRow ? ld_nc_v2(scales + r + (sub & 3) * 4) : make_uint2(0, 0);
         }
       };
-      int64_t rows = row_of(0, page_of(0)), next_rows = -1;
+      uint32_t rows = row_of(0, page_of(0)), next_rows = kNoRow;
       int page = -2;
       uint2 x[8], nx[8];
       load_scales(rows, x);
@@ -419,12 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             x[j].y &= 0x0000ffffu;
           }
           *reinterpret_cast<uint2*>(dst + 2 * kTile * L::kPd + kind * 2 * kTile + sub * 8) = x[j];
-          int64_t r[4];
+          uint32_t r[4];
           unsigned have = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             r[i] = __shfl_sync(kFullMask, rows, j * 4 + i);
-            have |= (r[i] >= 0 ? 1u : 0u) << i;
+            have |= (r[i] != kNoRow ? 1u : 0u) << i;
           }
           __syncwarp();
           if (tc5::elect_one()) {   // copies by several lanes at once take 100 cycles each
@@ -432,10 +434,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (r[i] < 0) continue;
-              bulk_g2s(dst + i * 16 * L::kPd, P.kc + r[i] * L::kPd, 16 * L::kPd, rawfull + st);
-              bulk_g2s(dst + (kTile + i * 16) * L::kPd, P.vc + r[i] * L::kPd, 16 * L::kPd,
-                       rawfull + st);
+              if (r[i] == kNoRow) continue;
+              const uint64_t at = static_cast<uint64_t>(r[i]) * L::kPd;
+              bulk_g2s(dst + i * 16 * L::kPd, P.kc + at, 16 * L::kPd, rawfull + st);
+              bulk_g2s(dst + (kTile + i * 16) * L::kPd, P.vc + at, 16 * L::kPd, rawfull + st);
             }
           }
           __syncwarp();
@@ -533,6 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           c[i].load(raw + row * L::kPd + src);
           s1[i] = sc[row];
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rawempty + st);   // all read: the next copies may come
         if (it >= 2) ok = warp_wait(empty + (it & 1), (it / 2 + 1) & 1, flags);
         if (!ok) break;
         unsigned char* dst = stages + (it & 1) * kStage;
@@ -570,10 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         if (found) flags[1] = 1;
         tc5::fence_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(full + (it & 1));
-          mbar_arrive(rawempty + st);
-        }
+        if (lane == 0) mbar_arrive(full + (it & 1));
       }
     }
   } else {
@@ -584,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       const Seq& q = g.u.q;
       const int node = g.u.r * a.tpt + ri;
       const bool live = ri < a.tpt && node < q.n;
+      const bool idle = !__any_sync(kFullMask, live);
       const int64_t row = (static_cast<int64_t>(g.u.l) * a.total + q.n0 + node) * a.Hq +
                           g.u.h * a.G + (r - ri * a.G);
       // Q of this row into TMEM, channels in the stored order
@@ -636,6 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         ok = warp_wait(sfull + (it & 1), (it >> 1) & 1, flags);
         if (!ok) break;
         tc5::fence_after();
+        if (idle) {   // no row of this warp is used: its weights may be anything
+          if (lane == 0) mbar_arrive(pready + (it & 1));
+          continue;
+        }
         const uint32_t sb = lanes + kColS + (it & 1) * kTile;
         const int t0 = (g.u.tile + j) * kTile;
         uint32_t s[kTile];
@@ -658,15 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             if (!(v1 >> i & 1)) s[32 + i] = 0xff800000u;
           }
         }
-        float mx0 = kNegInf, mx1 = kNegInf, mx2 = kNegInf, mx3 = kNegInf;
-#pragma unroll
-        for (int i = 0; i < kTile; i += 4) {
-          mx0 = fmaxf(mx0, __uint_as_float(s[i]));
-          mx1 = fmaxf(mx1, __uint_as_float(s[i + 1]));
-          mx2 = fmaxf(mx2, __uint_as_float(s[i + 2]));
-          mx3 = fmaxf(mx3, __uint_as_float(s[i + 3]));
-        }
-        const float x = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.c;
+        const float x = tc5::row_max<kTile>(s) * a.c;
         if (j == 0) {
           m = x;
         } else {
@@ -691,23 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           }
         }
         const float mo = m == kNegInf ? 0.f : m - tc5::kOff;
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) {
-            const float p0 = ex2_fast(fmaf(__uint_as_float(s[b * 32 + i]), a.c, -mo));
-            const float p1 = ex2_fast(fmaf(__uint_as_float(s[b * 32 + i + 1]), a.c, -mo));
-            const float p2 = ex2_fast(fmaf(__uint_as_float(s[b * 32 + i + 2]), a.c, -mo));
-            const float p3 = ex2_fast(fmaf(__uint_as_float(s[b * 32 + i + 3]), a.c, -mo));
-            l0 += p0; l1 += p1; l2 += p2; l3 += p3;
-            p[i / 2] = pack_h2(p0, p1);
-            p[i / 2 + 1] = pack_h2(p2, p3);
-          }
-          tc5::st16(sb + b * 16, p);
-        }
-        l += (l0 + l1) + (l2 + l3);
+        l += tc5::weights<false, kTile>(s, a.c, mo, sb);
         tc5::wait_st();
         tc5::fence_before();
         __syncwarp();
