@@ -221,34 +221,34 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// The weights 2^(s c - mo) of N scores, rounded to 16 bits, to the TMEM columns from `to` on;
-// returns their float32 sum.  Two elements per multiply-add and per addition (packed float32).
-template <bool BF, int N>
-__device__ __forceinline__ float weights(const uint32_t s[N], float c, float mo, uint32_t to) {
+// The weights 2^(s c - mo) of 32 scores, rounded to 16 bits, to the 16 TMEM columns from `to` on;
+// their float32 sums are added to the four in sum[2].  Two elements per multiply-add and per
+// addition (packed float32).
+template <bool BF>
+__device__ __forceinline__ void weights32(const uint32_t s[32], float c, float mo, uint32_t to,
+                                          uint64_t sum[2]) {
   const uint64_t c2 = pair(__float_as_uint(c), __float_as_uint(c));
   const uint64_t m2 = pair(__float_as_uint(-mo), __float_as_uint(-mo));
-  uint64_t sum0 = 0, sum1 = 0;
+  uint32_t p[16];
 #pragma unroll
-  for (int b = 0; b < N / 32; ++b) {
-    uint32_t p[16];
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-      float x0, x1, x2, x3;
-      unpair(fma2(pair(s[b * 32 + i], s[b * 32 + i + 1]), c2, m2), x0, x1);
-      unpair(fma2(pair(s[b * 32 + i + 2], s[b * 32 + i + 3]), c2, m2), x2, x3);
-      x0 = ex2_fast(x0);
-      x1 = ex2_fast(x1);
-      x2 = ex2_fast(x2);
-      x3 = ex2_fast(x3);
-      sum0 = add2(sum0, pair(__float_as_uint(x0), __float_as_uint(x1)));
-      sum1 = add2(sum1, pair(__float_as_uint(x2), __float_as_uint(x3)));
-      p[i / 2] = pack2<BF>(x0, x1);
-      p[i / 2 + 1] = pack2<BF>(x2, x3);
-    }
-    st16(to + b * 16, p);
+  for (int i = 0; i < 32; i += 4) {
+    float x0, x1, x2, x3;
+    unpair(fma2(pair(s[i], s[i + 1]), c2, m2), x0, x1);
+    unpair(fma2(pair(s[i + 2], s[i + 3]), c2, m2), x2, x3);
+    x0 = ex2_fast(x0);
+    x1 = ex2_fast(x1);
+    x2 = ex2_fast(x2);
+    x3 = ex2_fast(x3);
+    sum[0] = add2(sum[0], pair(__float_as_uint(x0), __float_as_uint(x1)));
+    sum[1] = add2(sum[1], pair(__float_as_uint(x2), __float_as_uint(x3)));
+    p[i / 2] = pack2<BF>(x0, x1);
+    p[i / 2 + 1] = pack2<BF>(x2, x3);
   }
+  st16(to, p);
+}
+__device__ __forceinline__ float sum_of(const uint64_t sum[2]) {
   float a, b;
-  unpair(add2(sum0, sum1), a, b);
+  unpair(add2(sum[0], sum[1]), a, b);
   return a + b;
 }
 

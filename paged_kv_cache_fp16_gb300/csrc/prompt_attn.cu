@@ -402,7 +402,10 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         }
       }
       const float mo = m == kNegInf ? 0.f : m - tc5::kOff;
-      l += tc5::weights<BF, NB>(s, a.c, mo, sb);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int q = 0; q < NB / 32; ++q) tc5::weights32<BF>(s + q * 32, a.c, mo, sb + q * 16, sum);
+      l += tc5::sum_of(sum);
       tc5::wait_st();
       if (edge) {
         // a slot's phase is told by its parity: the load before the one waited for must be known

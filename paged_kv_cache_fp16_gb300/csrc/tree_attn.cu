@@ -5,15 +5,15 @@
 // of 64 tokens the packed codes are brought in once and become fp16 in shared memory, exactly as
 // the dequantizer rounds them (k_hat = fp16(c * scale)):
 //   S = Q K_hat^T       tcgen05.mma, Q (fp16) in TMEM, K_hat in shared memory
-//   p = 2^(S c - m)     one thread per row, running maximum and sum; drafts outside the row's
+//   p = 2^(S c - m)     two threads per row, running maximum and sum; drafts outside the row's
 //                       64-bit ancestor mask get weight 0
 //   O += P V_hat        tcgen05.mma, P (fp16) in TMEM over the place of S, V_hat in shared memory
 // TMEM is full: O 256 columns, two score buffers of 64, Q 128.  With Q in TMEM the first product
 // reads only K_hat from shared memory, whose bandwidth is the scarcest after the codes' arrival.
 //
-// Roles of the 14 warps of a persistent CTA (one per SM): 4 softmax, 1 issues the products, 1
-// issues bulk copies of codes and scales (16-token groups of a page) into a ring deep enough to
-// cover the memory latency, 8 unpack.
+// Roles of the 26 warps of a persistent CTA (one per SM): 8 softmax, 1 issues the products, 1
+// brings codes and scales (16-token groups of a page) into a ring deep enough to cover the memory
+// latency, 16 unpack.
 //
 // Work: the tiles of all (layer, sequence, KV head, row tile) units in one line are dealt to the
 // CTAs in equal contiguous shares, whatever the sequences' lengths (which only the device knows).
@@ -42,8 +42,8 @@ namespace {
 constexpr int kD = 256;
 constexpr int kRows = 128;
 constexpr int kTile = 64;             // tokens per tile
-constexpr int kSoftmaxWarps = 4;      // warps 0-3; one arrival per warp: arrivals of lanes queue up
-constexpr int kMmaWarp = 4, kCopyWarp = 5, kUnpackWarp0 = 6, kUnpackWarps = 8;
+constexpr int kSoftmaxWarps = 8;      // warps 0-7: two threads per row, half of the columns each
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kUnpackWarp0 = 10, kUnpackWarps = 8;
 constexpr int kThreads = (kUnpackWarp0 + kUnpackWarps) * 32;
 constexpr int kRec = (kD + 2) * kRows;   // a partial record: O [256 / 4][128 rows][4], then m and l [128]
 constexpr int kShortTiles = 8;        // caches of at most so many tiles are not cut
@@ -60,6 +60,12 @@ struct TreePools {
   int64_t k_pages, v_pages;
 };
 
+// What a CTA leaves of the unit that its share cuts at the tail (the unit's first record): the
+// join needs no search.  n = 0: none.
+struct Cut {
+  int n, row0, stride, tokens;   // records from this CTA on; first row of out, rows per draft, drafts
+};
+
 struct TreeArgs {
   TreePools L[KVQ_MAX_TENSORS];
   const uint16_t* q;
@@ -74,6 +80,7 @@ struct TreeArgs {
   int tpt;      // drafts per row tile
   int grid;     // CTAs of the attention kernel
   int whole;    // deal whole units (short caches)
+  Cut* cuts;    // [grid]
   float c;      // softmax_scale * log2(e)
 };
 
@@ -87,7 +94,8 @@ struct Lay {
   static constexpr int kNumBars = 2 * kRaws + 4 * 2 + 3 * 2 + 2;
   static constexpr int kTail = kBars + kNumBars * 8;         // then: TMEM address, flags, meta,
   static constexpr int kParents = kTail + 16 + kMeta * 4;    // and the parents
-  static constexpr int kTotal = kParents + KVQ_MAX_NODES * 4;
+  static constexpr int kHalves = kParents + KVQ_MAX_NODES;       // and the exchange [2][128]
+  static constexpr int kTotal = kHalves + 2 * kRows * 4;
   static_assert(kTotal <= 232448, "shared memory");
 };
 
@@ -330,10 +338,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::kTail);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_ptr + 1);   // [0] gave up, [1] V
   volatile int* meta = reinterpret_cast<volatile int*>(sm + L::kTail + 16);
-  int* parents = reinterpret_cast<int*>(sm + L::kParents);
+  signed char* parents = reinterpret_cast<signed char*>(sm + L::kParents);
+  float* halves = reinterpret_cast<float*>(sm + L::kHalves);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Walk w = walk_of(a, blockIdx.x == 0 && warp == 0);
+  if (!w.whole && warp == kCopyWarp) {
+    // the unit that holds this share's last tile, if it starts here and ends behind the share
+    Cut cut{0, 0, 0, 0};
+    if (w.at < w.end) {
+      const Unit u = find_unit<true>(a, w.end - 1, w.layer_tiles, w.layer_units);
+      if (u.start >= w.at && u.start + u.q.tiles > w.end)
+        cut = Cut{static_cast<int>((u.start + u.q.tiles - 1) / share_of(a, w.layer_tiles)) -
+                      static_cast<int>(blockIdx.x) + 1,
+                  (u.l * a.total + u.q.n0 + u.r * a.tpt) * a.Hq + u.h * a.G, a.Hq,
+                  min(a.tpt, u.q.n - u.r * a.tpt)};
+    }
+    if (lane == 0) a.cuts[blockIdx.x] = cut;
+  }
   if (w.at >= w.end) return;
 
   if (threadIdx.x == 0) {
@@ -366,87 +388,106 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     // ------------------------------------------------------------------------- copies
     // Eight tiles at a time: lane i looks up the page of 16-token group i, then all lanes read
     // those tiles' scales (lane = K or V, four tokens; scales of tokens that are not there become
-    // 0, so that their rows unpack to zeros).  The next eight are looked up while the tiles of
-    // the present ones go out, one bulk copy per group for each of K and V codes.
+    // 0, so that their rows unpack to zeros).  The next eight, of the next segment too, are looked
+    // up while the tiles of the present ones go out, one bulk copy per group for each of K and V
+    // codes.
     const int kind = lane >> 4, sub = lane & 15;
-    while (ok && next_segment(a, w, g)) {
-      const TreePools& P = a.L[g.u.l];
-      const int total = g.u.q.len + g.u.q.n;
-      const uint16_t* scales = kind ? P.vs : P.ks;
-      auto page_of = [&](int b) {   // group `lane` of the tiles b .. b + 7 of the segment
-        const int tg = (g.u.tile + b) * kTile + lane * 16;
-        if (b + (lane >> 2) >= g.count || tg >= total) return -2;
-        const int lp = tg / a.ps;
-        return lp < a.max_pages ? __ldg(a.pt + static_cast<int64_t>(g.u.s) * a.max_pages + lp) : -1;
-      };
-      // Row numbers fit 32 bits: 2^32 - 1 rows of 128 bytes are more than the device's memory.
-      auto row_of = [&](int b, int page) -> uint32_t {
-        if (page == -2) return kNoRow;
-        if (page < 0 || page >= P.k_pages || page >= P.v_pages) {
-          report(a.err, KVQ_DEVERR_PAGE_RANGE);
-          return kNoRow;
+    struct Batch {
+      int first, total, n, l, h, s;   // first token, end of the sequence, tiles, unit
+    };
+    int b = 0;
+    bool more = next_segment(a, w, g);
+    auto next_batch = [&]() {
+      Batch x{0, 0, 0, 0, 0, 0};
+      if (more) {
+        x = Batch{(g.u.tile + b) * kTile, g.u.q.len + g.u.q.n, min(8, g.count - b), g.u.l, g.u.h,
+                  g.u.s};
+        b += 8;
+        if (b >= g.count) {
+          b = 0;
+          more = next_segment(a, w, g);
         }
-        const int tg = (g.u.tile + b) * kTile + lane * 16;
-        return (static_cast<uint32_t>(page) * a.H + g.u.h) * a.ps + tg % a.ps;
-      };
-      auto load_scales = [&](uint32_t rows, uint2 x[8]) {
+      }
+      return x;
+    };
+    auto page_of = [&](const Batch& x) {   // of group `lane`
+      const int tg = x.first + lane * 16;
+      if ((lane >> 2) >= x.n || tg >= x.total) return -2;
+      const int lp = tg / a.ps;
+      return lp < a.max_pages ? __ldg(a.pt + static_cast<int64_t>(x.s) * a.max_pages + lp) : -1;
+    };
+    // Row numbers fit 32 bits: 2^32 - 1 rows of 128 bytes are more than the device's memory.
+    auto row_of = [&](const Batch& x, int page) -> uint32_t {
+      if (page == -2) return kNoRow;
+      if (page < 0 || page >= a.L[x.l].k_pages || page >= a.L[x.l].v_pages) {
+        report(a.err, KVQ_DEVERR_PAGE_RANGE);
+        return kNoRow;
+      }
+      const int tg = x.first + lane * 16;
+      return (static_cast<uint32_t>(page) * a.H + x.h) * a.ps + tg % a.ps;
+    };
+    auto load_scales = [&](const Batch& x, uint32_t rows, uint2 v[8]) {
+      const uint16_t* scales = kind ? a.L[x.l].vs : a.L[x.l].ks;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t r = __shfl_sync(kFullMask, rows, j * 4 + (sub >> 2));
-          x[j] = r != kNoRow ? ld_nc_v2(scales + r + (sub & 3) * 4) : make_uint2(0, 0);
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t r = __shfl_sync(kFullMask, rows, j * 4 + (sub >> 2));
+        v[j] = r != kNoRow ? ld_nc_v2(scales + r + (sub & 3) * 4) : make_uint2(0, 0);
+      }
+    };
+    Batch cur = next_batch();
+    uint32_t rows = row_of(cur, page_of(cur));
+    uint2 x[8], nx[8];
+    load_scales(cur, rows, x);
+    while (ok && cur.n > 0) {
+      const uint8_t *kc = a.L[cur.l].kc, *vc = a.L[cur.l].vc;
+      Batch nxt = next_batch();
+      const int page = page_of(nxt);
+      uint32_t next_rows = kNoRow;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j == 4 || (j == 0 && cur.n <= 4)) {
+          next_rows = row_of(nxt, page);
+          load_scales(nxt, next_rows, nx);
         }
-      };
-      uint32_t rows = row_of(0, page_of(0)), next_rows = kNoRow;
-      int page = -2;
-      uint2 x[8], nx[8];
-      load_scales(rows, x);
-      for (int b = 0; ok && b < g.count; b += 8) {
+        if (!ok || j >= cur.n) continue;
+        const int st = it % R;
+        if (it >= R) ok = warp_wait(rawempty + st, (it / R + 1) & 1, flags);
+        if (!ok) continue;
+        unsigned char* dst = sm + L::kRawAt + st * L::kRaw;
+        const int left = cur.total - (cur.first + j * kTile + sub * 4);   // tokens still there
+        if (left < 4) {
+          if (left < 1) x[j].x &= 0xffff0000u;
+          if (left < 2) x[j].x &= 0x0000ffffu;
+          if (left < 3) x[j].y &= 0xffff0000u;
+          x[j].y &= 0x0000ffffu;
+        }
+        *reinterpret_cast<uint2*>(dst + 2 * kTile * L::kPd + kind * 2 * kTile + sub * 8) = x[j];
+        uint32_t r[4];
+        unsigned have = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j == 0) page = page_of(b + 8);
-          if (j == 4) {
-            next_rows = row_of(b + 8, page);
-            load_scales(next_rows, nx);
-          }
-          if (!ok || b + j >= g.count) continue;
-          const int st = it % R;
-          if (it >= R) ok = warp_wait(rawempty + st, (it / R + 1) & 1, flags);
-          if (!ok) continue;
-          unsigned char* dst = sm + L::kRawAt + st * L::kRaw;
-          const int left = total - ((g.u.tile + b + j) * kTile + sub * 4);   // tokens still there
-          if (left < 4) {
-            if (left < 1) x[j].x &= 0xffff0000u;
-            if (left < 2) x[j].x &= 0x0000ffffu;
-            if (left < 3) x[j].y &= 0xffff0000u;
-            x[j].y &= 0x0000ffffu;
-          }
-          *reinterpret_cast<uint2*>(dst + 2 * kTile * L::kPd + kind * 2 * kTile + sub * 8) = x[j];
-          uint32_t r[4];
-          unsigned have = 0;
+        for (int i = 0; i < 4; ++i) {
+          r[i] = __shfl_sync(kFullMask, rows, j * 4 + i);
+          have |= (r[i] != kNoRow ? 1u : 0u) << i;
+        }
+        __syncwarp();
+        if (tc5::elect_one()) {   // copies by several lanes at once take 100 cycles each
+          meta[it % kMeta] = static_cast<int>(have);
+          mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            r[i] = __shfl_sync(kFullMask, rows, j * 4 + i);
-            have |= (r[i] != kNoRow ? 1u : 0u) << i;
+            if (r[i] == kNoRow) continue;
+            const uint64_t at = static_cast<uint64_t>(r[i]) * L::kPd;
+            bulk_g2s(dst + i * 16 * L::kPd, kc + at, 16 * L::kPd, rawfull + st);
+            bulk_g2s(dst + (kTile + i * 16) * L::kPd, vc + at, 16 * L::kPd, rawfull + st);
           }
-          __syncwarp();
-          if (tc5::elect_one()) {   // copies by several lanes at once take 100 cycles each
-            meta[it % kMeta] = static_cast<int>(have);
-            mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (r[i] == kNoRow) continue;
-              const uint64_t at = static_cast<uint64_t>(r[i]) * L::kPd;
-              bulk_g2s(dst + i * 16 * L::kPd, P.kc + at, 16 * L::kPd, rawfull + st);
-              bulk_g2s(dst + (kTile + i * 16) * L::kPd, P.vc + at, 16 * L::kPd, rawfull + st);
-            }
-          }
-          __syncwarp();
-          ++it;
         }
-        rows = next_rows;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = nx[j];
+        __syncwarp();
+        ++it;
       }
+      cur = nxt;
+      rows = next_rows;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = nx[j];
     }
     if (!ok) {   // wait for the copies in flight
       for (int i = max(0, it - R); i < it; ++i) mbar_wait_bounded(rawfull + i % R, (i / R) & 1);
@@ -507,17 +548,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     }
   } else if (warp >= kUnpackWarp0) {
     // ------------------------------------------------------------------------------- unpack
-    // Four warps for K and four for V, so that neither waits for the other's products.  A warp's
+    // Half the warps for K and half for V, so that neither waits for the other's products.  A warp's
     // step takes two rows: lanes 8q .. 8q+7 hold panel q (64 channels) of both, four 16-channel
     // units each, which spreads a quarter-warp's 16-byte stores over all banks.  A tile's codes
     // are all read before the first is stored: reads and stores would otherwise alternate, each
     // waiting for the other.
-    const int kv = (warp - kUnpackWarp0) >> 2, uw = (warp - kUnpackWarp0) & 3;
+    constexpr int W = kUnpackWarps / 2;
+    const int kv = (warp - kUnpackWarp0) / W, uw = (warp - kUnpackWarp0) % W;
     const int q = lane >> 3, rr = (lane >> 2) & 1, u = lane & 3;
     const int src = (q * 4 + u) * 2 * BITS;
     uint64_t *full = kv ? vfull : kfull, *empty = kv ? vempty : kempty;
     unsigned char* stages = sm + (kv ? L::kV : L::kK) + q * kTile * 128;
-    constexpr int S = kTile / 8;   // steps: 16 rows per warp
+    constexpr int S = kTile / 2 / W;   // steps
     while (ok && next_segment(a, w, g)) {
       const int len = g.u.q.len;
       for (int j = 0; j < g.count; ++j, ++it) {
@@ -531,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         uint32_t s1[S];
 #pragma unroll
         for (int i = 0; i < S; ++i) {
-          const int row = (i * 4 + uw) * 2 + rr;
+          const int row = (i * W + uw) * 2 + rr;
           c[i].load(raw + row * L::kPd + src);
           s1[i] = sc[row];
         }
@@ -552,12 +594,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           for (int i = 0; i < S; ++i) {
             uint32_t o[8];
             c[i].unpack(s1[i] | (s1[i] << 16), o);
-            store((i * 4 + uw) * 2 + rr, o);
+            store((i * W + uw) * 2 + rr, o);
           }
         } else {   // drafts among the values: 0 * inf must not reach the rows that do not see them
 #pragma unroll
           for (int i = 0; i < S; ++i) {
-            const int row = (i * 4 + uw) * 2 + rr;
+            const int row = (i * W + uw) * 2 + rr;
             uint32_t o[8];
             c[i].unpack(s1[i] | (s1[i] << 16), o);
             if (t0 + row >= len) {
@@ -578,9 +620,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       }
     }
   } else {
-    // ------------------------------------------------------------------ softmax: thread = row
-    const int r = threadIdx.x, ri = r / a.G;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp) << 21);
+    // ------------------------------------- softmax: two threads per row, half the columns each
+    const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane, ri = r / a.G;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad) << 21);
+    // the other half's value, through shared memory: the row's two warps meet after the write and
+    // after the read
+    auto other = [&](float v) {
+      halves[half * kRows + r] = v;
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+      v = halves[(half ^ 1) * kRows + r];
+      asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+      return v;
+    };
     while (ok && next_segment(a, w, g)) {
       const Seq& q = g.u.q;
       const int node = g.u.r * a.tpt + ri;
@@ -590,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
                           g.u.h * a.G + (r - ri * a.G);
       // Q of this row into TMEM, channels in the stored order
 #pragma unroll 1
-      for (int b = 0; b < kD / 64; ++b) {
+      for (int b = half * 2; b < half * 2 + 2; ++b) {
         uint32_t x[32];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -620,16 +671,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       uint64_t seen = 0;
       const bool drafts = (g.u.tile + g.count) * kTile > q.len;
       if (drafts) {
-        asm volatile("bar.sync 1, 128;" ::: "memory");   // the previous unit's are no longer read
-        if (r < q.n) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");   // the previous unit's are no longer read
+        if (half == 0 && r < q.n) {
           int p = __ldg(a.parents + q.n0 + r);
           if (p < -1 || p >= r) {
             report(a.err, KVQ_DEVERR_INDEX);
             p = -1;
           }
-          parents[r] = p;
+          parents[r] = static_cast<signed char>(p);
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
+        asm volatile("bar.sync 1, 256;" ::: "memory");
         if (live)
           for (int i = node; i >= 0; i = parents[i]) seen |= 1ull << i;
       }
@@ -644,31 +695,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
         const uint32_t sb = lanes + kColS + (it & 1) * kTile;
         const int t0 = (g.u.tile + j) * kTile;
-        uint32_t s[kTile];
-        tc5::ld32(sb, s);
-        tc5::ld32(sb + 32, s + 32);
+        uint32_t s[32];
+        tc5::ld32(sb + half * 32, s);
         const unsigned have = static_cast<unsigned>(meta[it % kMeta]);
         tc5::wait_ld32(s);
-        tc5::after_ld32(s + 32);
         if (t0 + kTile > q.len || have != 15u) {
           const int d0 = t0 - q.len;   // node number of the tile's first token
-          uint64_t vis = d0 >= 0 ? (d0 < 64 ? seen >> d0 : 0)
-                       : d0 > -64 ? (seen << -d0) | ((1ull << -d0) - 1) : ~0ull;
+          uint64_t v = d0 >= 0 ? (d0 < 64 ? seen >> d0 : 0)
+                     : d0 > -64 ? (seen << -d0) | ((1ull << -d0) - 1) : ~0ull;
 #pragma unroll
           for (int gi = 0; gi < 4; ++gi)
-            if (!(have >> gi & 1)) vis &= ~(0xffffull << (16 * gi));
-          const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
+            if (!(have >> gi & 1)) v &= ~(0xffffull << (16 * gi));
+          const uint32_t vis = static_cast<uint32_t>(v >> (32 * half));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (!(v0 >> i & 1)) s[i] = 0xff800000u;
-            if (!(v1 >> i & 1)) s[32 + i] = 0xff800000u;
-          }
+          for (int i = 0; i < 32; ++i)
+            if (!(vis >> i & 1)) s[i] = 0xff800000u;
         }
-        const float x = tc5::row_max<kTile>(s) * a.c;
+        float x = tc5::row_max<32>(s) * a.c;
+        x = fmaxf(x, other(x));
         if (j == 0) {
           m = x;
         } else {
-          const bool up = x > m + tc5::kSlack;
+          const bool up = x > m + tc5::kSlack;   // the same in both halves
           if (__any_sync(kFullMask, up)) {
             const float f = up ? ex2_fast(m - x) : 1.f;
             if (up) m = x;
@@ -677,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             if (!ok) break;
             tc5::fence_after();
 #pragma unroll 1
-            for (int b = 0; b < kD / 32; ++b) {
+            for (int b = half * 4; b < half * 4 + 4; ++b) {
               uint32_t o[32];
               tc5::ld32(lanes + b * 32, o);
               tc5::wait_ld32(o);
@@ -689,7 +737,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           }
         }
         const float mo = m == kNegInf ? 0.f : m - tc5::kOff;
-        l += tc5::weights<false, kTile>(s, a.c, mo, sb);
+        uint64_t sum[2] = {0, 0};
+        // both halves' scores have been read (the exchange above), so the weights may go over them
+        tc5::weights32<false>(s, a.c, mo, sb + half * 16, sum);
+        l += tc5::sum_of(sum);
         tc5::wait_st();
         tc5::fence_before();
         __syncwarp();
@@ -699,13 +750,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       ok = warp_wait(odone + ((it - 1) & 1), (it - 1) >> 1 & 1, flags);
       if (!ok) break;
       tc5::fence_after();
+      l += other(l);
       const bool whole = g.count == q.tiles;
       const bool fix = drafts && flags[1] != 0;
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       // a cut unit at the head of the share is its first record, one at the tail its second
       float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (g.u.tile > 0 ? 0 : 1)) * kRec;
 #pragma unroll 1
-      for (int b = 0; b < kD / 32; ++b) {
+      for (int b = half * 4; b < half * 4 + 4; ++b) {
         uint32_t o[32];
         __syncwarp();
         tc5::ld32(lanes + b * 32, o);
@@ -749,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             dst[i * kRows] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         }
       }
-      if (live && !whole) {
+      if (live && !whole && half == 0) {
         part[kD * kRows + r] = m;
         part[(kD + 1) * kRows + r] = l;
       }
@@ -774,25 +826,30 @@ constexpr int kJoinCols = 8, kJoinSlices = 4;
 __global__ void __launch_bounds__(kRows * kJoinSlices)
 tree_join_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ float part_sm[kJoinSlices][kJoinCols + 2][kRows];
-  uint32_t tiles, units;
-  layer_totals(a, false, tiles, units);
-  if (blockIdx.x >= units * a.n_layers) return;
-  const Unit u = find_unit<false>(a, blockIdx.x, tiles, units);
-  if (u.s < 0) return;
-  const uint32_t share = share_of(a, tiles);
-  const int c0 = static_cast<int>(u.start / share);
-  const int c1 = static_cast<int>((u.start + u.q.tiles - 1) / share);
-  if (c0 == c1) return;   // finished by its CTA
+  // the block's unit: the blockIdx.x-th CTA that left a cut one
+  __shared__ int counts[kRows * kJoinSlices / 32], mine;
+  const bool has = threadIdx.x < a.grid && a.cuts[threadIdx.x].n > 0;
+  const unsigned votes = __ballot_sync(kFullMask, has);
+  if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = __popc(votes);
+  if (threadIdx.x == 0) mine = -1;
+  __syncthreads();
+  int rank = __popc(votes & ((1u << (threadIdx.x & 31)) - 1));
+  for (int i = 0; i < static_cast<int>(threadIdx.x >> 5); ++i) rank += counts[i];
+  if (has && rank == static_cast<int>(blockIdx.x)) mine = threadIdx.x;
+  __syncthreads();
+  if (mine < 0) return;
+  const Cut cut = a.cuts[mine];
+  const int c0 = mine, c1 = c0 + cut.n - 1;
   const int r = threadIdx.x % kRows, slice = threadIdx.x / kRows, col = blockIdx.y * kJoinCols;
-  const int ri = r / a.G, node = u.r * a.tpt + ri;
-  const bool live = ri < a.tpt && node < u.q.n;
+  const int ri = r / a.G;
+  const bool live = ri < cut.tokens;
   float M = kNegInf, l = 0.f, O[kJoinCols];
 #pragma unroll
   for (int e = 0; e < kJoinCols; ++e) O[e] = 0.f;
   if (live) {
 #pragma unroll 4
     for (int c = c0 + slice; c <= c1; c += kJoinSlices) {
-      // the unit's start lies in c0's share, so its record is the tail one there
+      // its first record is the tail one of c0, the others the head ones
       const float* p = a.ws + (static_cast<int64_t>(c) * 2 + (c == c0 ? 1 : 0)) * kRec;
       const float mi = p[kD * kRows + r], li = p[(kD + 1) * kRows + r];
       float4 o4[kJoinCols / 4];
@@ -828,12 +885,14 @@ tree_join_kernel(const __grid_constant__ TreeArgs a) {
     for (int e = 0; e < kJoinCols; ++e) O[e] = fmaf(part_sm[i][e][r], f, O[e]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t row = (static_cast<int64_t>(u.l) * a.total + u.q.n0 + node) * a.Hq + u.h * a.G +
-                      (r - ri * a.G);
+  const int64_t row = static_cast<int64_t>(cut.row0) + ri * cut.stride + (r - ri * a.G);
   uint32_t y[kJoinCols / 2];
 #pragma unroll
   for (int e = 0; e < kJoinCols; e += 2) y[e / 2] = pack_h2(O[e] * inv, O[e + 1] * inv);
-  *reinterpret_cast<uint4*>(a.out + row * kD + col) = make_uint4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+  for (int e = 0; e < kJoinCols / 8; ++e)
+    *reinterpret_cast<uint4*>(a.out + row * kD + col + e * 8) =
+        make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
 }
 
 // How a call is cut; the units are an upper bound (the lengths are on the device).
@@ -851,7 +910,8 @@ Plan plan_for(int n_layers, int nseq, int total_nodes, int H, int Hq, int max_no
   p.units = (a < b ? a : b) * H * n_layers;
   const int64_t tiles = (static_cast<int64_t>(max_len) + kTile - 1) / kTile;
   p.whole = tiles <= kShortTiles;
-  const int sms = sm_count() > 0 ? sm_count() : 152;
+  int sms = sm_count() > 0 ? sm_count() : 152;
+  if (sms > kRows * kJoinSlices) sms = kRows * kJoinSlices;   // the join's block looks at all CTAs
   const int64_t work = p.whole ? p.units : p.units * tiles;
   p.grid = static_cast<int>(work < sms ? (work < 1 ? 1 : work) : sms);
   return p;
@@ -866,8 +926,8 @@ cudaError_t launch(const TreeArgs& a, const Plan& p, cudaStream_t cs) {
   tree_attn_kernel<BITS><<<p.grid, kThreads, Lay<BITS>::kTotal, cs>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.whole) return e;
-  tree_join_kernel<<<dim3(static_cast<unsigned>(p.units), kD / kJoinCols), kRows * kJoinSlices, 0,
-                     cs>>>(a);
+  const unsigned cuts = static_cast<unsigned>(p.units < p.grid ? p.units : p.grid);
+  tree_join_kernel<<<dim3(cuts, kD / kJoinCols), kRows * kJoinSlices, 0, cs>>>(a);
   return cudaGetLastError();
 }
 
@@ -886,7 +946,7 @@ extern "C" size_t kvq_tree_attn_workspace(int n_layers, int nseq, int total_node
   const kvq::Plan p = kvq::plan_for(n_layers, nseq, total_nodes, num_kv_heads, num_q_heads,
                                     max_nodes, max_seq_len);
   if (p.whole) return 16;
-  return static_cast<size_t>(p.grid) * 2 * kvq::kRec * sizeof(float);
+  return static_cast<size_t>(p.grid) * (2 * kvq::kRec * sizeof(float) + sizeof(kvq::Cut));
 }
 
 extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_pools, int n_layers,
@@ -952,6 +1012,7 @@ extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_p
   a.n_layers = n_layers; a.nseq = nseq; a.total = total_nodes; a.H = H; a.Hq = num_q_heads;
   a.G = num_q_heads / H; a.ps = k0.page_size; a.max_pages = max_pages; a.max_nodes = max_nodes;
   a.max_len = max_seq_len; a.tpt = p.tpt; a.grid = p.grid; a.whole = p.whole ? 1 : 0;
+  a.cuts = reinterpret_cast<Cut*>(a.ws + static_cast<int64_t>(p.grid) * 2 * kRec);
   a.c = softmax_scale * 1.4426950408889634f;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = k0.bits == 8 ? launch<8>(a, p, cs)
