@@ -10,6 +10,7 @@ Build it with ``python -c "import __graft_entry__ as g; g.build()"`` or
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass
@@ -744,45 +745,67 @@ KVQ_F16, KVQ_BF16 = 0, 1
 _DTYPES = {torch.float16: KVQ_F16, torch.bfloat16: KVQ_BF16}
 
 
-def _here(t, name: str, dtype=None, dims: int | None = None):
-    """A contiguous tensor of the current device (the one whose stream the call uses)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _device(t, name: str) -> int:
+    """The index of the device a call works on: `t`'s, which must be the current one (the one
+    whose stream the call uses)."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return dev
+
+
+def _here(t, name: str, dev: int, dtype=None, dims: int | None = None) -> int:
+    """The address of a contiguous tensor of device `dev`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dims is not None and t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions")
-    return t
+    return t.data_ptr()
 
 
-def _head_rows(t, name: str, like=None) -> int:
-    """Checks [tokens, heads, D] rows of 16-bit values, a token's heads contiguous, and returns the
-    elements between tokens."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _opt(t, name: str, dev: int, dtype, dims: int | None = None) -> int | None:
+    return None if t is None else _here(t, name, dev, dtype, dims)
+
+
+def _head_rows(t, name: str, dev: int, dtype) -> tuple[int, int]:
+    """Checks [tokens, heads, D] rows of `dtype`, a token's heads contiguous, and returns their
+    address and the elements between tokens."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPES or (like is not None and t.dtype != like.dtype):
-        raise TypeError(f"{name} must be float16 or bfloat16, all alike, got {t.dtype}")
-    if t.device.index != torch.cuda.current_device():
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    sn, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.stride(0) if n > 1 else -(-h * d // 8) * 8
+    return t.data_ptr(), (sn if n > 1 else -(-h * d // 8) * 8)
 
 
-def _opt(t, name: str, dtype, dims: int | None = None):
-    return None if t is None else _here(t, name, dtype, dims).data_ptr()
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _workspace(t) -> tuple[int, int]:
-    _here(t, "workspace")
-    return t.data_ptr(), t.numel() * t.element_size()
+def _pool_structs(pools: Sequence[Pool], dev: int) -> ctypes.Array:
+    """The pools as an array of kvq_pool (five 64-bit words each)."""
+    words = []
+    for p in pools:
+        if p.codes.get_device() != dev or p.scales.get_device() != dev:
+            raise ValueError("the pools are not on the current device")
+        words += (p.bits & 0xffffffff | p.num_heads << 32, p.head_dim & 0xffffffff | p.page_size << 32,
+                  p.codes.shape[0], p.codes.data_ptr(), p.scales.data_ptr())
+    return (kvq_pool * len(pools)).from_buffer(array.array("Q", words))
 
 
 def kvq_rope_phases(inv_freq, device="cuda") -> torch.Tensor:
@@ -801,26 +824,31 @@ def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_out: torch.Tensor, k_ou
     """Norm (where a weight is given) and position rotation (over 2 * phases.numel() channels) of
     every row of q [tokens, Hq, D] and k [tokens, H, D] into q_out, k_out (q and k themselves to
     work in place).  fp16 or bf16; tokens may be strided (views of a fused projection)."""
-    qs, ks = _head_rows(q, "q"), _head_rows(k, "k", q)
-    qos, kos = _head_rows(q_out, "q_out", q), _head_rows(k_out, "k_out", q)
+    dev, dt = _device(q, "q"), q.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"q must be float16 or bfloat16, got {dt}")
+    qp, qs = _head_rows(q, "q", dev, dt)
+    kp, ks = _head_rows(k, "k", dev, dt)
+    qop, qos = (qp, qs) if q_out is q else _head_rows(q_out, "q_out", dev, dt)
+    kop, kos = (kp, ks) if k_out is k else _head_rows(k_out, "k_out", dev, dt)
     if q_out.shape != q.shape or k_out.shape != k.shape:
         raise ValueError("q_out / k_out must have q's / k's shape")
     n, hq, d = q.shape
     if k.shape[0] != n or k.shape[2] != d:
         raise ValueError("q and k must have the same tokens and head_dim")
-    _here(positions, "positions", torch.int32, 1)
-    if positions.shape[0] != n:
+    if positions.shape != (n,):
         raise ValueError("one position per token")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.numel() != d:
+        if w is not None and w.shape != (d,):
             raise ValueError(f"{name} must have head_dim entries")
-    _check(_lib.kvq_qk_norm_rope(_DTYPES[q.dtype], q.data_ptr(), qs, k.data_ptr(), ks,
-                                 q_out.data_ptr(), qos, k_out.data_ptr(), kos, n, hq, k.shape[1],
+    _check(_lib.kvq_qk_norm_rope(_DTYPES[dt], qp, qs, kp, ks, qop, qos, kop, kos, n, hq, k.shape[1],
                                  d, 0 if phases is None else 2 * phases.numel(),
-                                 1 if interleaved else 0, positions.data_ptr(),
-                                 _opt(phases, "phases", torch.int64, 1),
-                                 _opt(q_weight, "q_weight", torch.float32),
-                                 _opt(k_weight, "k_weight", torch.float32), eps, _stream(stream)))
+                                 1 if interleaved else 0,
+                                 _here(positions, "positions", dev, torch.int32),
+                                 _opt(phases, "phases", dev, torch.int64, 1),
+                                 _opt(q_weight, "q_weight", dev, torch.float32),
+                                 _opt(k_weight, "k_weight", dev, torch.float32), eps,
+                                 _raw_stream(stream, dev)))
 
 
 def kvq_prompt_attn_workspace(nseq: int, total_q: int, num_q_heads: int, num_kv_heads: int,
@@ -843,25 +871,32 @@ def kvq_prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     """Causal attention of packed sequences: q [total_q, Hq, D] over k, v [total_k, H, D] (fp16 or
     bf16, tokens may be strided) into out [total_q, Hq, D] (contiguous), row statistics into lse
     float32 [total_q, Hq]."""
-    qs, ks, vs = _head_rows(q, "q"), _head_rows(k, "k", q), _head_rows(v, "v", q)
-    if k.shape != v.shape or k.shape[2] != q.shape[2]:
+    dev, dt = _device(q, "q"), q.dtype
+    if dt not in _DTYPES:
+        raise TypeError(f"q must be float16 or bfloat16, got {dt}")
+    qp, qs = _head_rows(q, "q", dev, dt)
+    kp, ks = _head_rows(k, "k", dev, dt)
+    vp, vs = _head_rows(v, "v", dev, dt)
+    n, hq, d = q.shape
+    total_k, h, dk = k.shape
+    if k.shape != v.shape or dk != d:
         raise ValueError("k and v must have one shape, and q's head_dim")
-    _here(out, "out", q.dtype)
     if out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    _here(cu_q, "cu_q", torch.int32, 1)
-    _here(cu_k, "cu_k", torch.int32, 1)
-    if cu_q.shape[0] < 1 or cu_k.shape != cu_q.shape:
+    nseq = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
+    if nseq < 0 or cu_k.shape != cu_q.shape:
         raise ValueError("cu_q and cu_k must have nseq + 1 entries each")
-    n, hq, d = q.shape
     if lse is not None and lse.shape != (n, hq):
         raise ValueError("lse must be [total_q, Hq]")
-    ws, ws_bytes = _workspace(workspace)
-    _check(_lib.kvq_prompt_attn(_DTYPES[q.dtype], q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(),
-                                vs, hq, k.shape[1], d, cu_q.data_ptr(), cu_k.data_ptr(),
-                                cu_q.shape[0] - 1, n, k.shape[0], max_q, max_k, softmax_scale,
-                                out.data_ptr(), _opt(lse, "lse", torch.float32), ws, ws_bytes,
-                                _opt(dev_err, "dev_err", torch.int32), _stream(stream)))
+    _check(_lib.kvq_prompt_attn(_DTYPES[dt], qp, qs, kp, ks, vp, vs, hq, h, d,
+                                _here(cu_q, "cu_q", dev, torch.int32),
+                                _here(cu_k, "cu_k", dev, torch.int32), nseq, n, total_k, max_q,
+                                max_k, softmax_scale, _here(out, "out", dev, dt),
+                                _opt(lse, "lse", dev, torch.float32),
+                                _here(workspace, "workspace", dev),
+                                workspace.numel() * workspace.element_size(),
+                                _opt(dev_err, "dev_err", dev, torch.int32),
+                                _raw_stream(stream, dev)))
 
 
 # --------------------------------------------------------------------- trees of drafted tokens
@@ -882,13 +917,11 @@ def tree_workspace(k_pools: Sequence[Pool], nseq: int, total_nodes: int, num_q_h
 
 
 def _tree_table(page_table, seq_lens, cu) -> int:
-    """Checks the tensors that describe the sequences of a tree call; returns their count."""
-    _here(page_table, "page_table", torch.int32, 2)
-    _here(seq_lens, "seq_lens", torch.int32, 1)
-    nseq = seq_lens.shape[0]
-    if page_table.shape[0] < nseq or cu.dim() != 1 or cu.shape[0] != nseq + 1:
+    """Checks the shapes of what describes a tree call's sequences; returns their count."""
+    if seq_lens.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] < seq_lens.shape[0] \
+            or cu.shape != (seq_lens.shape[0] + 1,):
         raise ValueError("page_table needs a row per sequence and the offsets nseq + 1 entries")
-    return nseq
+    return seq_lens.shape[0]
 
 
 def kvq_tree_attn(k_pools: Sequence[Pool], v_pools: Sequence[Pool], q: torch.Tensor,
@@ -901,22 +934,26 @@ def kvq_tree_attn(k_pools: Sequence[Pool], v_pools: Sequence[Pool], q: torch.Ten
     max_seq_len bounds seq_lens plus the drafts."""
     if len(k_pools) != len(v_pools):
         raise ValueError("one V pool per K pool")
-    _here(q, "q", torch.float16, 4)
-    _here(out, "out", torch.float16)
-    _here(cu_nodes, "cu_nodes", torch.int32)
-    _here(parents, "parents", torch.int32, 1)
-    nseq = _tree_table(page_table, seq_lens, cu_nodes)
+    dev = _device(q, "q")
+    if q.dim() != 4:
+        raise ValueError("q must be [n_layers, total_nodes, Hq, D]")
     n_layers, total, hq, d = q.shape
-    if n_layers != len(k_pools) or out.shape != q.shape or parents.shape[0] != total:
+    if n_layers != len(k_pools) or out.shape != q.shape or parents.shape != (total,):
         raise ValueError("q and out are [n_layers, total_nodes, Hq, D], with a parent per node")
     if d != k_pools[0].head_dim:
         raise ValueError("q and the pools must have one head_dim")
-    ws, ws_bytes = _workspace(workspace)
-    _check(_lib.kvq_tree_attn(_pool_array(k_pools), _pool_array(v_pools), n_layers, q.data_ptr(),
-                              hq, page_table.data_ptr(), page_table.shape[1], seq_lens.data_ptr(),
-                              cu_nodes.data_ptr(), parents.data_ptr(), nseq, total, max_nodes,
-                              max_seq_len, softmax_scale, out.data_ptr(), ws, ws_bytes,
-                              _opt(dev_err, "dev_err", torch.int32), _stream(stream)))
+    nseq = _tree_table(page_table, seq_lens, cu_nodes)
+    _check(_lib.kvq_tree_attn(_pool_structs(k_pools, dev), _pool_structs(v_pools, dev), n_layers,
+                              _here(q, "q", dev, torch.float16), hq,
+                              _here(page_table, "page_table", dev, torch.int32),
+                              page_table.shape[1], _here(seq_lens, "seq_lens", dev, torch.int32),
+                              _here(cu_nodes, "cu_nodes", dev, torch.int32),
+                              _here(parents, "parents", dev, torch.int32), nseq, total, max_nodes,
+                              max_seq_len, softmax_scale, _here(out, "out", dev, torch.float16),
+                              _here(workspace, "workspace", dev),
+                              workspace.numel() * workspace.element_size(),
+                              _opt(dev_err, "dev_err", dev, torch.int32),
+                              _raw_stream(stream, dev)))
 
 
 def kvq_tree_commit(pools: Sequence[Pool], page_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -924,13 +961,16 @@ def kvq_tree_commit(pools: Sequence[Pool], page_table: torch.Tensor, seq_lens: t
                     dev_err: torch.Tensor | None = None, stream=None) -> None:
     """Move the accepted drafts (node numbers accept[cu_accept[s]:cu_accept[s + 1]]) to the places
     behind seq_lens[s], in every pool.  seq_lens is not advanced."""
-    _here(cu_accept, "cu_accept", torch.int32)
-    _here(accept, "accept", torch.int32, 1)
+    dev = _device(accept, "accept")
     nseq = _tree_table(page_table, seq_lens, cu_accept)
-    _check(_lib.kvq_tree_commit(_pool_array(pools), len(pools), page_table.data_ptr(),
-                                page_table.shape[1], seq_lens.data_ptr(), cu_accept.data_ptr(),
-                                accept.data_ptr(), nseq, accept.shape[0],
-                                _opt(dev_err, "dev_err", torch.int32), _stream(stream)))
+    _check(_lib.kvq_tree_commit(_pool_structs(pools, dev), len(pools),
+                                _here(page_table, "page_table", dev, torch.int32),
+                                page_table.shape[1],
+                                _here(seq_lens, "seq_lens", dev, torch.int32),
+                                _here(cu_accept, "cu_accept", dev, torch.int32),
+                                _here(accept, "accept", dev, torch.int32, 1), nseq,
+                                accept.shape[0], _opt(dev_err, "dev_err", dev, torch.int32),
+                                _raw_stream(stream, dev)))
 
 
 __all__ = ["KVQError", "Pool", "Allocator", "parse_mode", "kvq_version", "kvq_packed_dim",
