@@ -7,10 +7,16 @@
 // once per token and used by all of its heads, which leaves two multiply-adds and one multiply
 // per element of a row.
 //
-// A row is held by D / 8 lanes (8 channels = 16 bytes each; the next power of two of lanes is set
-// aside for it, so a warp holds 1, 2 or 4 rows of 256, 128 or 64 channels).  The mean is a
-// shuffle tree over those lanes; the partner's values come by four more shuffles of the packed
-// words (pairs half a row apart) or are the lane's own (interleaved).
+// A row is held by D / 8 lanes, 8 channels each (the next power of two of lanes is set aside for
+// it, so a warp holds 1, 2 or 4 rows of 256, 128 or 64 channels).  A lane's channels are two runs
+// of 4 so chosen that both channels of a pair are its own: for pairs half a rotated part apart,
+// one run from each half; a row then costs two 8-byte loads and stores and no exchange but the
+// mean's shuffle tree.
+//
+// What bounds it is the arithmetic as much as the memory: 32,768 tokens of 28 rows of 256 channels
+// (940 MB) would take 139 us at the copy rate.  Measured there: with the partner's channels
+// fetched by shuffles and 16-byte loads 202 us (126 registers, 2 blocks per SM), see the launch
+// bounds below for this form.
 //
 // The angle in turns is position * phase mod 2^64 with the phase in units of 2^-64 turn: exact to
 // 2^-33 turn for every 32-bit position.  Its sine and cosine are the hardware approximations of
@@ -26,6 +32,7 @@
 
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "kvq_tc5.cuh"
 
 namespace kvq {
 namespace {
@@ -45,15 +52,11 @@ struct NormRopeArgs {
   int rows_per_task, tasks_per_token;
 };
 
-__device__ __forceinline__ uint4 ld_v4(const void* p) {
-  return *reinterpret_cast<const uint4*>(p);
-}
-
 template <bool BF>
-__device__ __forceinline__ void unpack8(const uint4& v, float x[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack4(const uint2& v, float x[4]) {
+  const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     if constexpr (BF) {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
@@ -65,129 +68,133 @@ __device__ __forceinline__ void unpack8(const uint4& v, float x[8]) {
   }
 }
 
-template <bool BF>
-__device__ __forceinline__ uint4 pack8(const float x[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (BF) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    } else {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// What a lane keeps for one token: its channels' own and partner factors, and where its partner is.
-template <int LPR, bool INTER>
+// Where a lane's two runs of 4 channels start, and what their pairs turn by.
 struct Lane {
-  int sub;        // lane within the row
-  bool live;      // holds channels (sub * 8 < D)
-  bool rot;       // its channels are rotated (8 at a time: rotary_dim is a multiple of 16)
-  int src;        // the lane that holds the partners
-  float c[8], s[8];
+  int a, b;       // channels a .. a+3 and b .. b+3
+  int pair0;      // its first pair's number
+  bool live;      // holds channels
+  bool rot;       // they are rotated (8 at a time: rotary_dim is a multiple of 16)
 };
 
-template <int LPR, bool INTER>
-__device__ __forceinline__ void token_factors(Lane<LPR, INTER>& L, const NormRopeArgs& a, int t) {
-  const int64_t p = __ldg(a.pos + t);
-  const int half = a.rd >> 1, d0 = L.sub * 8;
+// The factors of a lane's outputs: with INTER pairs are (x0, x1), (x2, x3) of each run and
+//   y_e = x_e own[e] + x_(e^1) part[e];
+// otherwise (x_e, x_(e+4)), e < 4, and the partner of e is e ^ 4.
+template <bool INTER>
+__device__ __forceinline__ void factors(const Lane& L, const float c[4], const float s[4],
+                                        const float* w, uint64_t own[4], uint64_t part[4]) {
+  float wt[8], o[8], p[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) { L.c[e] = 1.f; L.s[e] = 0.f; }
-  if (!L.rot) return;
-  const int i0 = INTER ? (d0 >> 1) : (d0 < half ? d0 : d0 - half);
-  const bool second = !INTER && d0 >= half;
+  for (int e = 0; e < 8; ++e)
+    wt[e] = w != nullptr && L.live ? __ldg(w + (e < 4 ? L.a + e : L.b + e - 4)) : 1.f;
 #pragma unroll
-  for (int i = 0; i < (INTER ? 4 : 8); ++i) {
-    const uint64_t turn = static_cast<uint64_t>(p) * __ldg(a.phases + i0 + i) + 0x80000000ull;
-    const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) *
-                    1.4629180792671596e-9f;   // 2 pi / 2^32
-    const float c = __cosf(x), s = __sinf(x);
-    if constexpr (INTER) {
-      L.c[2 * i] = L.c[2 * i + 1] = c;
-      L.s[2 * i] = -s;
-      L.s[2 * i + 1] = s;
-    } else {
-      L.c[i] = c;
-      L.s[i] = second ? s : -s;
+  for (int e = 0; e < 8; ++e) {
+    const int i = INTER ? e >> 1 : e & 3, q = INTER ? e ^ 1 : e ^ 4;
+    const bool first = INTER ? !(e & 1) : e < 4;
+    o[e] = wt[e] * c[i];
+    p[e] = first ? -(wt[q] * s[i]) : wt[q] * s[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    own[i] = tc5::pair(__float_as_uint(o[2 * i]), __float_as_uint(o[2 * i + 1]));
+    part[i] = tc5::pair(__float_as_uint(p[2 * i]), __float_as_uint(p[2 * i + 1]));
+  }
+}
+
+// The rows [0, n) at x (D apart) to y; NORM: divided by their root mean square.
+template <bool BF, int LPR, bool INTER, bool NORM>
+__device__ __forceinline__ void rows(const Lane& L, const NormRopeArgs& a, const uint16_t* x,
+                                     uint16_t* y, const uint64_t own[4], const uint64_t part[4],
+                                     int n, int n_max) {
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  constexpr int U = 4;   // rows in flight per group of lanes
+#pragma unroll 1
+  for (int r0 = 0; r0 < n_max; r0 += U) {
+    uint2 v[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v[u][0] = v[u][1] = make_uint2(0, 0);
+      if (L.live && r0 + u < n) {
+        const uint16_t* p = x + static_cast<int64_t>(r0 + u) * a.D;
+        v[u][0] = *reinterpret_cast<const uint2*>(p + L.a);
+        v[u][1] = *reinterpret_cast<const uint2*>(p + L.b);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[8];
+      unpack4<BF>(v[u][0], f);
+      unpack4<BF>(v[u][1], f + 4);
+      uint64_t f2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f2[i] = tc5::pair(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
+      uint64_t y2[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t o = tc5::mul2(f2[i], own[i]);
+        // the partners of elements 2i and 2i + 1
+        const uint64_t q = INTER ? tc5::pair(__float_as_uint(f[2 * i + 1]), __float_as_uint(f[2 * i]))
+                                 : f2[i ^ 2];
+        y2[i] = tc5::fma2(q, part[i], o);
+      }
+      if (!L.rot) {   // (a partner times 0 could still be a NaN)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y2[i] = tc5::mul2(f2[i], own[i]);
+      }
+      if constexpr (NORM) {
+        uint64_t ss2 = tc5::mul2(f2[0], f2[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) ss2 = tc5::fma2(f2[i], f2[i], ss2);
+        float s0, s1;
+        tc5::unpair(ss2, s0, s1);
+        float ss = s0 + s1;
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o, LPR);
+        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+        const uint64_t r2 = tc5::pair(__float_as_uint(r), __float_as_uint(r));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y2[i] = tc5::mul2(y2[i], r2);
+      }
+      if (L.live && r0 + u < n) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          tc5::unpair(y2[i], lo, hi);
+          w[i] = tc5::pack2<BF>(lo, hi);
+        }
+        uint16_t* p = y + static_cast<int64_t>(r0 + u) * a.D;
+        *reinterpret_cast<uint2*>(p + L.a) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(p + L.b) = make_uint2(w[2], w[3]);
+      }
     }
   }
 }
 
-// The rows [0, n) at x (D apart) to y, with the norm's weights w (NULL: no norm).
 template <bool BF, int LPR, bool INTER>
-__device__ __forceinline__ void rows(const Lane<LPR, INTER>& L, const NormRopeArgs& a,
-                                     const uint16_t* x, uint16_t* y, const float* w, int n,
-                                     int n_max) {
-  const int d0 = L.sub * 8;
-  float wc[8], ws[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) { wc[e] = L.c[e]; ws[e] = L.s[e]; }
-  if (w != nullptr && L.live) {
-    const int half = a.rd >> 1;
-    const int dp = INTER || !L.rot ? d0 : (d0 < half ? d0 + half : d0 - half);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      wc[e] *= __ldg(w + d0 + e);
-      ws[e] *= __ldg(w + (INTER ? (d0 + (e ^ 1)) : (dp + e)));
-    }
-  }
-  const float inv_d = 1.f / static_cast<float>(a.D);
-  constexpr int U = 4;   // rows in flight per group of lanes
-  for (int r0 = 0; r0 < n_max; r0 += U) {
-    uint4 v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (L.live && r0 + u < n) v[u] = ld_v4(x + static_cast<int64_t>(r0 + u) * a.D + d0);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float f[8], g[8];
-      unpack8<BF>(v[u], f);
-      float r = 1.f;
-      if (w != nullptr) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o, LPR);
-        r = rsqrtf(fmaf(ss, inv_d, a.eps));
-      }
-      if constexpr (INTER) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = L.rot ? f[e ^ 1] : 0.f;
-      } else {
-        uint4 pv;
-        pv.x = __shfl_sync(kFullMask, v[u].x, L.src, LPR);
-        pv.y = __shfl_sync(kFullMask, v[u].y, L.src, LPR);
-        pv.z = __shfl_sync(kFullMask, v[u].z, L.src, LPR);
-        pv.w = __shfl_sync(kFullMask, v[u].w, L.src, LPR);
-        if (!L.rot) pv = make_uint4(0, 0, 0, 0);   // a zero partner: 0 * 0 adds nothing
-        unpack8<BF>(pv, g);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = fmaf(g[e], ws[e], f[e] * wc[e]) * r;
-      if (L.live && r0 + u < n)
-        *reinterpret_cast<uint4*>(y + static_cast<int64_t>(r0 + u) * a.D + d0) = pack8<BF>(f);
-    }
-  }
+__device__ __forceinline__ void rows_of(const Lane& L, const NormRopeArgs& a, const float c[4],
+                                        const float s[4], const uint16_t* x, uint16_t* y,
+                                        const float* w, int n, int n_max) {
+  if (n_max == 0) return;
+  uint64_t own[4], part[4];
+  factors<INTER>(L, c, s, w, own, part);
+  if (w != nullptr) rows<BF, LPR, INTER, true>(L, a, x, y, own, part, n, n_max);
+  else rows<BF, LPR, INTER, false>(L, a, x, y, own, part, n, n_max);
 }
 
 // A task is one token and rows_per_task of its Hq + H rows; groups of LPR lanes take tasks in
 // turn.  Groups of one warp run the same number of steps, so every shuffle has all its lanes.
+// 64 registers and four blocks per SM: the loads in flight and the other warps' arithmetic cover
+// each other (2 blocks 203 us, 3 196 us, 4 192 us in the form with shuffles).
 template <bool BF, int LPR, bool INTER>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
-  Lane<LPR, INTER> L;
-  const int lane = threadIdx.x & 31;
-  L.sub = lane & (LPR - 1);
-  L.live = L.sub * 8 < a.D;
-  L.rot = L.sub * 8 < a.rd;
-  const int hl = a.rd >> 4;   // lanes per half of the rotated part
-  L.src = L.rot ? (L.sub < hl ? L.sub + hl : L.sub - hl) : L.sub;
+__global__ void __launch_bounds__(256, 4) norm_rope_kernel(const NormRopeArgs a) {
+  Lane L;
+  const int lane = threadIdx.x & 31, sub = lane & (LPR - 1), half = a.rd >> 1;
+  L.live = sub * 8 < a.D;
+  L.rot = sub * 8 < a.rd;
+  L.a = INTER || !L.rot ? sub * 8 : sub * 4;
+  L.b = INTER || !L.rot ? sub * 8 + 4 : half + sub * 4;
+  L.pair0 = sub * 4;
   constexpr int GPW = 32 / LPR;
   const int64_t n_tasks = static_cast<int64_t>(a.tokens) * a.tasks_per_token;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
@@ -200,19 +207,30 @@ __global__ void __launch_bounds__(256) norm_rope_kernel(const NormRopeArgs a) {
     const int r0 = static_cast<int>(tk - static_cast<int64_t>(t) * a.tasks_per_token) *
                    a.rows_per_task;
     const int r1 = min(r0 + a.rows_per_task, a.Hq + a.H);
-    token_factors(L, a, t);
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (L.rot) {
+      const int64_t p = __ldg(a.pos + t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t turn = static_cast<uint64_t>(p) * __ldg(a.phases + L.pair0 + i) + 0x80000000ull;
+        const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) *
+                        1.4629180792671596e-9f;   // 2 pi / 2^32
+        c[i] = __cosf(x);
+        s[i] = __sinf(x);
+      }
+    }
     const int q0 = min(r0, a.Hq), q1 = min(r1, a.Hq);
     const int k0 = max(r0, a.Hq) - a.Hq, k1 = max(r1, a.Hq) - a.Hq;
-    int nq = on ? q1 - q0 : 0, nk = on ? k1 - k0 : 0;
+    const int nq = on ? q1 - q0 : 0, nk = on ? k1 - k0 : 0;
     int mq = nq, mk = nk;
     if constexpr (GPW > 1) {
       mq = __reduce_max_sync(kFullMask, nq);
       mk = __reduce_max_sync(kFullMask, nk);
     }
-    rows<BF>(L, a, a.q + t * a.qs + static_cast<int64_t>(q0) * a.D,
-             a.qo + t * a.qos + static_cast<int64_t>(q0) * a.D, a.qw, nq, mq);
-    rows<BF>(L, a, a.k + t * a.ks + static_cast<int64_t>(k0) * a.D,
-             a.ko + t * a.kos + static_cast<int64_t>(k0) * a.D, a.kw, nk, mk);
+    rows_of<BF, LPR, INTER>(L, a, c, s, a.q + t * a.qs + static_cast<int64_t>(q0) * a.D,
+                            a.qo + t * a.qos + static_cast<int64_t>(q0) * a.D, a.qw, nq, mq);
+    rows_of<BF, LPR, INTER>(L, a, c, s, a.k + t * a.ks + static_cast<int64_t>(k0) * a.D,
+                            a.ko + t * a.kos + static_cast<int64_t>(k0) * a.D, a.kw, nk, mk);
   }
 }
 
@@ -297,7 +315,7 @@ extern "C" kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64
   const int sms = sm_count() > 0 ? sm_count() : 152;
   // Whole tokens per task when they fill the machine (the factors are then formed once per
   // token); with fewer, a token's rows go to several tasks, four at least (one batch of loads).
-  const int64_t slots = static_cast<int64_t>(sms) * 64 * (32 / lpr);   // groups resident at once
+  const int64_t slots = static_cast<int64_t>(sms) * 16 * (32 / lpr);   // half the groups resident at once
   const int total = num_q_heads + num_kv_heads;
   int64_t split = slots / num_tokens;
   const int most = (total + 3) / 4;
