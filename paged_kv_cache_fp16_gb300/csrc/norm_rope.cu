@@ -15,8 +15,7 @@
 //
 // What bounds it is the arithmetic as much as the memory: 32,768 tokens of 28 rows of 256 channels
 // (940 MB) would take 139 us at the copy rate.  Measured there: with the partner's channels
-// fetched by shuffles and 16-byte loads 202 us (126 registers, 2 blocks per SM), see the launch
-// bounds below for this form.
+// fetched by shuffles and 16-byte loads 202 us (126 registers, 2 blocks per SM), in this form 155.
 //
 // The angle in turns is position * phase mod 2^64 with the phase in units of 2^-64 turn: exact to
 // 2^-33 turn for every 32-bit position.  Its sine and cosine are the hardware approximations of
@@ -52,19 +51,16 @@ struct NormRopeArgs {
   int rows_per_task, tasks_per_token;
 };
 
+// Two 16-bit values as float32.
 template <bool BF>
-__device__ __forceinline__ void unpack4(const uint2& v, float x[4]) {
-  const uint32_t w[2] = {v.x, v.y};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if constexpr (BF) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
+__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
+  if constexpr (BF) {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xffff0000u);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = f.x;
+    hi = f.y;
   }
 }
 
@@ -76,22 +72,22 @@ struct Lane {
   bool rot;       // they are rotated (8 at a time: rotary_dim is a multiple of 16)
 };
 
-// The factors of a lane's outputs: with INTER pairs are (x0, x1), (x2, x3) of each run and
-//   y_e = x_e own[e] + x_(e^1) part[e];
-// otherwise (x_e, x_(e+4)), e < 4, and the partner of e is e ^ 4.
+// A lane's 8 values are held as the first of its four pairs, then the second (e < 4 and e >= 4):
+// with INTER pair i is the neighbours 2i, 2i + 1 of its 8 channels, otherwise one value of each
+// run.  The factors: y_e = x_e own[e] + x_(e^4) part[e].
 template <bool INTER>
 __device__ __forceinline__ void factors(const Lane& L, const float c[4], const float s[4],
                                         const float* w, uint64_t own[4], uint64_t part[4]) {
   float wt[8], o[8], p[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    wt[e] = w != nullptr && L.live ? __ldg(w + (e < 4 ? L.a + e : L.b + e - 4)) : 1.f;
+    wt[e] = w != nullptr && L.live
+                ? __ldg(w + (INTER ? L.a + 2 * (e & 3) + (e >> 2) : e < 4 ? L.a + e : L.b + e - 4))
+                : 1.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int i = INTER ? e >> 1 : e & 3, q = INTER ? e ^ 1 : e ^ 4;
-    const bool first = INTER ? !(e & 1) : e < 4;
-    o[e] = wt[e] * c[i];
-    p[e] = first ? -(wt[q] * s[i]) : wt[q] * s[i];
+    o[e] = wt[e] * c[e & 3];
+    p[e] = e < 4 ? -(wt[e + 4] * s[e]) : wt[e - 4] * s[e - 4];
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -100,43 +96,55 @@ __device__ __forceinline__ void factors(const Lane& L, const float c[4], const f
   }
 }
 
-// The rows [0, n) at x (D apart) to y; NORM: divided by their root mean square.
+constexpr int kThreads = 128;
+constexpr int kU = 4;   // rows in flight per group of lanes
+
+// Rows r0 .. r0 + kU - 1 of the n at x (D apart).
+__device__ __forceinline__ void load_rows(const Lane& L, const NormRopeArgs& a, const uint16_t* x,
+                                          int r0, int n, uint2 v[kU][2]) {
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    v[u][0] = v[u][1] = make_uint2(0, 0);
+    if (L.live && r0 + u < n) {
+      const uint16_t* p = x + static_cast<int64_t>(r0 + u) * a.D;
+      v[u][0] = *reinterpret_cast<const uint2*>(p + L.a);
+      v[u][1] = *reinterpret_cast<const uint2*>(p + L.b);
+    }
+  }
+}
+
+// The rows [0, n) at x, of which v holds the first batch, to y; NORM: divided by their root mean
+// square.
 template <bool BF, int LPR, bool INTER, bool NORM>
 __device__ __forceinline__ void rows(const Lane& L, const NormRopeArgs& a, const uint16_t* x,
                                      uint16_t* y, const uint64_t own[4], const uint64_t part[4],
-                                     int n, int n_max) {
+                                     int n, int n_max, uint2 v[kU][2]) {
   const float inv_d = 1.f / static_cast<float>(a.D);
-  constexpr int U = 4;   // rows in flight per group of lanes
 #pragma unroll 1
-  for (int r0 = 0; r0 < n_max; r0 += U) {
-    uint2 v[U][2];
+  for (int r0 = 0; r0 < n_max; r0 += kU) {
+    if (r0 > 0) load_rows(L, a, x, r0, n, v);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      v[u][0] = v[u][1] = make_uint2(0, 0);
-      if (L.live && r0 + u < n) {
-        const uint16_t* p = x + static_cast<int64_t>(r0 + u) * a.D;
-        v[u][0] = *reinterpret_cast<const uint2*>(p + L.a);
-        v[u][1] = *reinterpret_cast<const uint2*>(p + L.b);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kU; ++u) {
       float f[8];
-      unpack4<BF>(v[u][0], f);
-      unpack4<BF>(v[u][1], f + 4);
+      if constexpr (INTER) {
+        unpack2<BF>(v[u][0].x, f[0], f[4]);
+        unpack2<BF>(v[u][0].y, f[1], f[5]);
+        unpack2<BF>(v[u][1].x, f[2], f[6]);
+        unpack2<BF>(v[u][1].y, f[3], f[7]);
+      } else {
+        unpack2<BF>(v[u][0].x, f[0], f[1]);
+        unpack2<BF>(v[u][0].y, f[2], f[3]);
+        unpack2<BF>(v[u][1].x, f[4], f[5]);
+        unpack2<BF>(v[u][1].y, f[6], f[7]);
+      }
       uint64_t f2[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         f2[i] = tc5::pair(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
       uint64_t y2[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint64_t o = tc5::mul2(f2[i], own[i]);
-        // the partners of elements 2i and 2i + 1
-        const uint64_t q = INTER ? tc5::pair(__float_as_uint(f[2 * i + 1]), __float_as_uint(f[2 * i]))
-                                 : f2[i ^ 2];
-        y2[i] = tc5::fma2(q, part[i], o);
-      }
+      for (int i = 0; i < 4; ++i)
+        y2[i] = tc5::fma2(f2[i ^ 2], part[i], tc5::mul2(f2[i], own[i]));
       if (!L.rot) {   // (a partner times 0 could still be a NaN)
 #pragma unroll
         for (int i = 0; i < 4; ++i) y2[i] = tc5::mul2(f2[i], own[i]);
@@ -156,13 +164,13 @@ __device__ __forceinline__ void rows(const Lane& L, const NormRopeArgs& a, const
         for (int i = 0; i < 4; ++i) y2[i] = tc5::mul2(y2[i], r2);
       }
       if (L.live && r0 + u < n) {
+        float g[8];
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float lo, hi;
-          tc5::unpair(y2[i], lo, hi);
-          w[i] = tc5::pack2<BF>(lo, hi);
-        }
+        for (int i = 0; i < 4; ++i) tc5::unpair(y2[i], g[2 * i], g[2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = INTER ? tc5::pack2<BF>(g[i], g[i + 4]) : tc5::pack2<BF>(g[2 * i], g[2 * i + 1]);
         uint16_t* p = y + static_cast<int64_t>(r0 + u) * a.D;
         *reinterpret_cast<uint2*>(p + L.a) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2*>(p + L.b) = make_uint2(w[2], w[3]);
@@ -174,20 +182,17 @@ __device__ __forceinline__ void rows(const Lane& L, const NormRopeArgs& a, const
 template <bool BF, int LPR, bool INTER>
 __device__ __forceinline__ void rows_of(const Lane& L, const NormRopeArgs& a, const float c[4],
                                         const float s[4], const uint16_t* x, uint16_t* y,
-                                        const float* w, int n, int n_max) {
-  if (n_max == 0) return;
+                                        const float* w, int n, int n_max, uint2 v[kU][2]) {
   uint64_t own[4], part[4];
   factors<INTER>(L, c, s, w, own, part);
-  if (w != nullptr) rows<BF, LPR, INTER, true>(L, a, x, y, own, part, n, n_max);
-  else rows<BF, LPR, INTER, false>(L, a, x, y, own, part, n, n_max);
+  if (w != nullptr) rows<BF, LPR, INTER, true>(L, a, x, y, own, part, n, n_max, v);
+  else rows<BF, LPR, INTER, false>(L, a, x, y, own, part, n, n_max, v);
 }
 
-// A task is one token and rows_per_task of its Hq + H rows; groups of LPR lanes take tasks in
-// turn.  Groups of one warp run the same number of steps, so every shuffle has all its lanes.
-// 64 registers and four blocks per SM: the loads in flight and the other warps' arithmetic cover
-// each other (2 blocks 203 us, 3 196 us, 4 192 us in the form with shuffles).
+// 64 registers and 32 warps per SM: loads in flight and other warps' arithmetic cover each other.
+// 32,768 tokens: 155 us, 6.05 TB/s (24 warps 162 us, 40 warps, which spill, 238 us).
 template <bool BF, int LPR, bool INTER>
-__global__ void __launch_bounds__(256, 4) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) norm_rope_kernel(const NormRopeArgs a) {
   Lane L;
   const int lane = threadIdx.x & 31, sub = lane & (LPR - 1), half = a.rd >> 1;
   L.live = sub * 8 < a.D;
@@ -196,17 +201,31 @@ __global__ void __launch_bounds__(256, 4) norm_rope_kernel(const NormRopeArgs a)
   L.b = INTER || !L.rot ? sub * 8 + 4 : half + sub * 4;
   L.pair0 = sub * 4;
   constexpr int GPW = 32 / LPR;
-  const int64_t n_tasks = static_cast<int64_t>(a.tokens) * a.tasks_per_token;
-  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t step = (static_cast<int64_t>(gridDim.x) * blockDim.x >> 5) * GPW;
-  for (int64_t base = warp * GPW; base < n_tasks; base += step) {
-    const int64_t task = base + lane / LPR;
+  // tasks fit 32 bits: a token has several only where tokens are few
+  const uint32_t n_tasks = static_cast<uint32_t>(a.tokens) * a.tasks_per_token;
+  const uint32_t warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const uint32_t step = (gridDim.x * blockDim.x >> 5) * GPW;
+  for (uint32_t base = warp * GPW; base < n_tasks; base += step) {
+    const uint32_t task = base + lane / LPR;
     const bool on = task < n_tasks;
-    const int64_t tk = on ? task : n_tasks - 1;
-    const int t = static_cast<int>(tk / a.tasks_per_token);
-    const int r0 = static_cast<int>(tk - static_cast<int64_t>(t) * a.tasks_per_token) *
+    const uint32_t tk = on ? task : n_tasks - 1;
+    const int t = a.tasks_per_token == 1 ? tk : tk / static_cast<uint32_t>(a.tasks_per_token);
+    const int r0 = static_cast<int>(tk - static_cast<uint32_t>(t) * a.tasks_per_token) *
                    a.rows_per_task;
     const int r1 = min(r0 + a.rows_per_task, a.Hq + a.H);
+    const int q0 = min(r0, a.Hq), q1 = min(r1, a.Hq);
+    const int k0 = max(r0, a.Hq) - a.Hq, k1 = max(r1, a.Hq) - a.Hq;
+    const int nq = on ? q1 - q0 : 0, nk = on ? k1 - k0 : 0;
+    int mq = nq, mk = nk;
+    if constexpr (GPW > 1) {
+      mq = __reduce_max_sync(kFullMask, nq);
+      mk = __reduce_max_sync(kFullMask, nk);
+    }
+    const uint16_t* xq = a.q + t * a.qs + static_cast<int64_t>(q0) * a.D;
+    const uint16_t* xk = a.k + t * a.ks + static_cast<int64_t>(k0) * a.D;
+    uint2 v[kU][2];   // the first rows are on their way while the factors are formed
+    if (mq > 0) load_rows(L, a, xq, 0, nq, v);
+    else load_rows(L, a, xk, 0, nk, v);
     float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
     if (L.rot) {
       const int64_t p = __ldg(a.pos + t);
@@ -219,25 +238,21 @@ __global__ void __launch_bounds__(256, 4) norm_rope_kernel(const NormRopeArgs a)
         s[i] = __sinf(x);
       }
     }
-    const int q0 = min(r0, a.Hq), q1 = min(r1, a.Hq);
-    const int k0 = max(r0, a.Hq) - a.Hq, k1 = max(r1, a.Hq) - a.Hq;
-    const int nq = on ? q1 - q0 : 0, nk = on ? k1 - k0 : 0;
-    int mq = nq, mk = nk;
-    if constexpr (GPW > 1) {
-      mq = __reduce_max_sync(kFullMask, nq);
-      mk = __reduce_max_sync(kFullMask, nk);
+    if (mq > 0) {
+      rows_of<BF, LPR, INTER>(L, a, c, s, xq, a.qo + t * a.qos + static_cast<int64_t>(q0) * a.D,
+                              a.qw, nq, mq, v);
+      if (mk > 0) load_rows(L, a, xk, 0, nk, v);
     }
-    rows_of<BF, LPR, INTER>(L, a, c, s, a.q + t * a.qs + static_cast<int64_t>(q0) * a.D,
-                            a.qo + t * a.qos + static_cast<int64_t>(q0) * a.D, a.qw, nq, mq);
-    rows_of<BF, LPR, INTER>(L, a, c, s, a.k + t * a.ks + static_cast<int64_t>(k0) * a.D,
-                            a.ko + t * a.kos + static_cast<int64_t>(k0) * a.D, a.kw, nk, mk);
+    if (mk > 0)
+      rows_of<BF, LPR, INTER>(L, a, c, s, xk, a.ko + t * a.kos + static_cast<int64_t>(k0) * a.D,
+                              a.kw, nk, mk, v);
   }
 }
 
 template <bool BF, int LPR>
 void launch(const NormRopeArgs& a, bool inter, int blocks, cudaStream_t cs) {
-  if (inter) norm_rope_kernel<BF, LPR, true><<<blocks, 256, 0, cs>>>(a);
-  else norm_rope_kernel<BF, LPR, false><<<blocks, 256, 0, cs>>>(a);
+  if (inter) norm_rope_kernel<BF, LPR, true><<<blocks, kThreads, 0, cs>>>(a);
+  else norm_rope_kernel<BF, LPR, false><<<blocks, kThreads, 0, cs>>>(a);
 }
 
 template <bool BF>
@@ -315,7 +330,7 @@ extern "C" kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64
   const int sms = sm_count() > 0 ? sm_count() : 152;
   // Whole tokens per task when they fill the machine (the factors are then formed once per
   // token); with fewer, a token's rows go to several tasks, four at least (one batch of loads).
-  const int64_t slots = static_cast<int64_t>(sms) * 16 * (32 / lpr);   // half the groups resident at once
+  const int64_t slots = static_cast<int64_t>(sms) * 32 * (32 / lpr);   // groups resident at once
   const int total = num_q_heads + num_kv_heads;
   int64_t split = slots / num_tokens;
   const int most = (total + 3) / 4;
@@ -324,7 +339,9 @@ extern "C" kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64
   a.tasks_per_token = (total + a.rows_per_task - 1) / a.rows_per_task;
   const int64_t groups = static_cast<int64_t>(num_tokens) * a.tasks_per_token;
   const int64_t warps = (groups + 32 / lpr - 1) / (32 / lpr);
-  const int64_t want = (warps + 7) / 8, cap = static_cast<int64_t>(sms) * 8;
+  constexpr int kWarps = kThreads / 32;
+  const int64_t want = (warps + kWarps - 1) / kWarps;
+  const int64_t cap = static_cast<int64_t>(sms) * (64 / kWarps);
   const int blocks = static_cast<int>(want < cap ? want : cap);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == KVQ_BF16) launch_lanes<true>(a, interleaved != 0, lpr, blocks, cs);
