@@ -163,6 +163,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, i
       : "memory");
 }
 
+// The two warps (of 8 softmax warps) that share the rows of quadrant `quad` meet.  Barrier numbers
+// are spelt out: with a number in a register a kernel is charged all 16 of a block's barriers.
+__device__ __forceinline__ void meet(int quad) {
+  switch (quad) {
+    case 0: asm volatile("bar.sync 2, 64;" ::: "memory"); break;
+    case 1: asm volatile("bar.sync 3, 64;" ::: "memory"); break;
+    case 2: asm volatile("bar.sync 4, 64;" ::: "memory"); break;
+    default: asm volatile("bar.sync 5, 64;" ::: "memory"); break;
+  }
+}
+
 // ---- the online softmax of a row held by one thread ---------------------------------------------
 // Scores are taken to log2 units (x = s * scale * log2 e).  The row keeps a reference m that its
 // weights 2^(x - m + kOff) are taken against, moved to the true maximum only when that has grown

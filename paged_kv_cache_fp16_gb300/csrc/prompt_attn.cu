@@ -51,7 +51,7 @@ constexpr int kThreads = 192;
 // NS: score buffers.  kSlots: ring slots.  kCtas: resident CTAs per SM.
 template <int D> struct Cfg;
 template <> struct Cfg<256> { static constexpr int NB = 128, KD = 128, VR = 64, NS = 2, kSlots = 5, kCtas = 1; };
-template <> struct Cfg<128> { static constexpr int NB = 128, KD = 64, VR = 64, NS = 1, kSlots = 5, kCtas = 2; };
+template <> struct Cfg<128> { static constexpr int NB = 64, KD = 128, VR = 64, NS = 2, kSlots = 5, kCtas = 2; };
 template <> struct Cfg<64> { static constexpr int NB = 64, KD = 64, VR = 64, NS = 2, kSlots = 8, kCtas = 2; };
 
 template <int D>
@@ -64,7 +64,7 @@ struct Lay {
   static constexpr int kBars = kRing + C::kSlots * kSlot;
   static constexpr int kNumBars = 2 * C::kSlots + 3 + 2 * C::NS;
   static constexpr int kTotal = kBars + kNumBars * 8 + 16;
-  static constexpr int kCols = C::kCtas == 1 ? 512 : 256;
+  static constexpr int kCols = 512 / C::kCtas;
   static_assert(D + C::NS * C::NB <= kCols, "TMEM");
   static constexpr int nk = D / C::KD, nv = C::NB / C::VR;
 };
@@ -366,6 +366,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       const uint32_t sb = lanes + D + (j % NS) * NB;
       const int t0 = (j0 + j) * NB;
       const bool edge = t0 + NB > lim_min;
+      const int left = limit - t0;   // columns that the row sees
       uint32_t s[NB];
 #pragma unroll
       for (int q = 0; q < NB / 32; ++q) tc5::ld32(sb + q * 32, s + q * 32);
@@ -375,7 +376,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       if (edge) {
 #pragma unroll
         for (int i = 0; i < NB; ++i)
-          if (t0 + i >= limit) s[i] = 0xff800000u;
+          if (i >= left) s[i] = 0xff800000u;
       }
       const float x = tc5::row_max<NB>(s) * a.c;
       if (j == 0) {
@@ -404,7 +405,9 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       const float mo = m == kNegInf ? 0.f : m - tc5::kOff;
       uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int q = 0; q < NB / 32; ++q) tc5::weights32<BF>(s + q * 32, a.c, mo, sb + q * 16, sum);
+      for (int q = 0; q < NB / 32; ++q) {   // over the scores already read
+        tc5::weights32<BF>(s + q * 32, a.c, mo, sb + q * 16, sum);
+      }
       l += tc5::sum_of(sum);
       tc5::wait_st();
       if (edge) {
@@ -552,7 +555,7 @@ struct Plan {
 
 Plan plan_for(int nseq, int total_q, int num_q_heads, int num_kv_heads, int D, int max_q,
               int max_k) {
-  const int nb = D == 64 ? 64 : 128, ctas = D == 256 ? 1 : 2;
+  const int nb = D == 256 ? 128 : 64, ctas = D == 256 ? 1 : 2;
   Plan p;
   p.tpt = kRows / (num_q_heads / num_kv_heads);
   const int64_t per = (static_cast<int64_t>(max_q) + p.tpt - 1) / p.tpt;

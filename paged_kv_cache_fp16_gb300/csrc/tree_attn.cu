@@ -627,9 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     // after the read
     auto other = [&](float v) {
       halves[half * kRows + r] = v;
-      asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+      tc5::meet(quad);
       v = halves[(half ^ 1) * kRows + r];
-      asm volatile("bar.sync %0, 64;" ::"r"(2 + quad) : "memory");
+      tc5::meet(quad);
       return v;
     };
     while (ok && next_segment(a, w, g)) {
