@@ -91,14 +91,15 @@ struct Unit {
   bool found;
 };
 
-// The unit of linear index u, found by a whole warp: sequences in order, within one the KV heads,
-// within a head the tiles from the last (the most keys) to the first.  Sequences that contradict
+// The unit of linear index u, found by a whole warp: sequences in order, within one the tiles from
+// the last (the most keys) to the first, so that the CTAs that start last have the least to do, and
+// for each tile the KV heads.  Sequences that contradict
 // the call's bounds have none; with `check` set all of them are looked at and reported.
 __device__ __forceinline__ Unit find_unit(const PromptArgs& a, int u, bool check) {
   const int lane = threadIdx.x & 31;
   Unit r;
   r.found = false;
-  int64_t before = 0;
+  uint32_t before = 0;   // a call's units fit 31 bits
   for (int base = 0; base < a.nseq; base += 32) {
     const int s = base + lane;
     int q0 = 0, q1 = 0, k0 = 0, k1 = 0, tiles = 0;
@@ -112,25 +113,26 @@ __device__ __forceinline__ Unit find_unit(const PromptArgs& a, int u, bool check
       if (ok) tiles = (q1 - q0 + a.tpt - 1) / a.tpt;
       else if (check) report(a.err, KVQ_DEVERR_INDEX);
     }
-    const int64_t mine = static_cast<int64_t>(tiles) * a.H;
-    int64_t incl = mine;
+    const uint32_t mine = static_cast<uint32_t>(tiles) * a.H;
+    uint32_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(kFullMask, incl, o);
+      const uint32_t x = __shfl_up_sync(kFullMask, incl, o);
       if (lane >= o) incl += x;
     }
-    const int64_t start = before + incl - mine;
-    const unsigned hit = __ballot_sync(kFullMask, u >= start && u < start + mine);
+    const uint32_t start = before + incl - mine, at = static_cast<uint32_t>(u);
+    const unsigned hit = __ballot_sync(kFullMask, at >= start && at - start < mine);
     if (hit && !r.found) {
       const int src = __ffs(hit) - 1;
-      const int rem = __shfl_sync(kFullMask, static_cast<int>(u - start), src);
-      const int t = __shfl_sync(kFullMask, tiles, src);
+      const uint32_t rem = __shfl_sync(kFullMask, at - start, src);
+      const uint32_t t = __shfl_sync(kFullMask, tiles, src);
       r.q0 = __shfl_sync(kFullMask, q0, src);
       r.lq = __shfl_sync(kFullMask, q1, src) - r.q0;
       r.k0 = __shfl_sync(kFullMask, k0, src);
       r.lk = __shfl_sync(kFullMask, k1, src) - r.k0;
-      r.h = rem / t;
-      r.tile = t - 1 - (rem - r.h * t);
+      const uint32_t back = rem / a.H;
+      r.h = static_cast<int>(rem - back * a.H);
+      r.tile = static_cast<int>(t - 1 - back);
       r.found = true;
       if (!check) return r;
     }
@@ -502,49 +504,83 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
   if (threadIdx.x == 0 && flags[0]) report(a.err, KVQ_DEVERR_TIMEOUT);
 }
 
-// Joins the splits of a row: one warp per row of a unit; lane holds D / 32 channels.
-template <bool BF, int D>
-__global__ void __launch_bounds__(256) prompt_join_kernel(const __grid_constant__ PromptArgs a) {
-  constexpr int NB = Cfg<D>::NB, E = D / 32;
-  const int lane = threadIdx.x & 31;
+// Joins the splits of a unit's rows: a thread holds 4 channels of a row and of one of S slices of
+// the splits.  With up to 8 splits S = 1 and a block has several rows; with more, the slices of one
+// row are joined in shared memory (one warp per row with the splits one after the other took 11 us
+// for the 38 splits of a single token's rows; S > 1 for many rows of few splits took 10 us more
+// than S = 1).
+constexpr int kJoinThreads = 256;
+
+template <bool BF, int D, int S>
+__global__ void __launch_bounds__(kJoinThreads)
+prompt_join_kernel(const __grid_constant__ PromptArgs a) {
+  constexpr int NB = Cfg<D>::NB, T = D / 4, kRowsPer = kJoinThreads / (T * S);
+  __shared__ float4 so[S][T];
+  __shared__ float sm[S], sl[S];
   const Unit n = find_unit(a, blockIdx.x, false);
   if (!n.found) return;
   const int i0 = n.tile * a.tpt, i1 = min(i0 + a.tpt, n.lq);
   const int all = (keys_seen(n, i1 - 1) + NB - 1) / NB;
   if (all <= a.tps) return;
   const int live = (all + a.tps - 1) / a.tps;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int tok = i0 + r / a.G;
-  if (r >= (i1 - i0) * a.G) return;
-  const float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * a.n_splits * kRows + r) * (D + 4);
+  const int t = threadIdx.x % T, slice = S > 1 ? threadIdx.x / T : 0;
   constexpr int64_t step = static_cast<int64_t>(kRows) * (D + 4);
-  float M = kNegInf;
-  for (int i = lane; i < live; i += 32) M = fmaxf(M, part[i * step + D]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-  float O[E], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) O[e] = 0.f;
+  // (with S > 1 all threads of a block have one row)
+  for (int r = blockIdx.y * kRowsPer + (S > 1 ? 0 : threadIdx.x / T); r < (i1 - i0) * a.G;
+       r += gridDim.y * kRowsPer) {
+    const float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * a.n_splits * kRows + r) * (D + 4);
+    float M = kNegInf, l = 0.f;
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = 0; i < live; ++i) {
-    const float* p = part + i * step;
-    const float mi = p[D], f = mi == kNegInf ? 0.f : ex2_fast(mi - M);
-    l = fmaf(p[D + 1], f, l);
+    for (int i = slice; i < live; i += S) {
+      const float* p = part + i * step;
+      const float4 o = *reinterpret_cast<const float4*>(p + t * 4);
+      const float2 ml = *reinterpret_cast<const float2*>(p + D);
+      const float Mn = fmaxf(M, ml.x);
+      const float f = M == kNegInf ? 0.f : ex2_fast(M - Mn);
+      const float g = ml.x == kNegInf ? 0.f : ex2_fast(ml.x - Mn);
+      l = l * f + ml.y * g;
+      O.x = O.x * f + o.x * g;
+      O.y = O.y * f + o.y * g;
+      O.z = O.z * f + o.z * g;
+      O.w = O.w * f + o.w * g;
+      M = Mn;
+    }
+    if constexpr (S > 1) {
+      so[slice][t] = O;
+      if (t == 0) {
+        sm[slice] = M;
+        sl[slice] = l;
+      }
+      __syncthreads();
+      if (slice == 0) {
+        M = sm[0];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 o = *reinterpret_cast<const float2*>(p + e * 32 + lane * 2);
-      O[e] = fmaf(o.x, f, O[e]);
-      O[e + 1] = fmaf(o.y, f, O[e + 1]);
+        for (int i = 1; i < S; ++i) M = fmaxf(M, sm[i]);
+        l = 0.f;
+        O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+          const float g = sm[i] == kNegInf ? 0.f : ex2_fast(sm[i] - M);
+          const float4 o = so[i][t];
+          l = fmaf(sl[i], g, l);
+          O.x = fmaf(o.x, g, O.x);
+          O.y = fmaf(o.y, g, O.y);
+          O.z = fmaf(o.z, g, O.z);
+          O.w = fmaf(o.w, g, O.w);
+        }
+      }
+      __syncthreads();
+    }
+    if (slice == 0) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t row = (static_cast<int64_t>(n.q0) + i0 + r / a.G) * a.Hq + n.h * a.G + r % a.G;
+      *reinterpret_cast<uint2*>(a.out + row * D + t * 4) =
+          make_uint2(tc5::pack2<BF>(O.x * inv, O.y * inv), tc5::pack2<BF>(O.z * inv, O.w * inv));
+      if (a.lse && t == 0)
+        a.lse[row] = M == kNegInf ? kNegInf : (M - tc5::kOff + log2f(l)) * 0.6931471805599453f;
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t row = (static_cast<int64_t>(n.q0) + tok) * a.Hq + n.h * a.G + r % a.G;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(a.out + row * D + e * 32 + lane * 2) =
-        tc5::pack2<BF>(O[e] * inv, O[e + 1] * inv);
-  if (a.lse && lane == 0)
-    a.lse[row] = M == kNegInf ? kNegInf : (M - tc5::kOff + log2f(l)) * 0.6931471805599453f;
 }
 
 // How a call is cut: row tiles (an upper bound: the lengths are on the device) and splits.
@@ -631,8 +667,15 @@ kvq_status launch(const char* fn, PromptArgs& a, const Plan& p, const uint16_t* 
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && p.n_splits > 1) {
-    const int rows = a.G * (a.max_q < p.tpt ? a.max_q : p.tpt);
-    prompt_join_kernel<BF, D><<<dim3(static_cast<unsigned>(p.units), (rows + 7) / 8), 256, 0, cs>>>(a);
+    constexpr int kSlices = kJoinThreads / (D / 4);
+    const bool few = p.n_splits <= 8;
+    int blocks = a.G * (a.max_q < p.tpt ? a.max_q : p.tpt);   // rows of a unit
+    if (few) blocks = (blocks + kSlices - 1) / kSlices;
+    const int64_t fill = 8192 / p.units;   // a few waves at most
+    if (blocks > fill) blocks = fill < 1 ? 1 : static_cast<int>(fill);
+    const dim3 grid(static_cast<unsigned>(p.units), blocks);
+    if (few) prompt_join_kernel<BF, D, 1><<<grid, kJoinThreads, 0, cs>>>(a);
+    else prompt_join_kernel<BF, D, kSlices><<<grid, kJoinThreads, 0, cs>>>(a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, "%s launch: %s", fn, cudaGetErrorString(e));
