@@ -91,49 +91,84 @@ struct Unit {
   bool found;
 };
 
-// The unit of linear index u, found by a whole warp: sequences in order, within one the tiles from
-// the last (the most keys) to the first, so that the CTAs that start last have the least to do, and
-// for each tile the KV heads.  Sequences that contradict
-// the call's bounds have none; with `check` set all of them are looked at and reported.
+struct SeqSpan {
+  int q0, lq, k0, lk, tiles;
+};
+
+// Sequence s's offsets and row tiles (none if it contradicts the call's bounds).
+__device__ __forceinline__ SeqSpan span_of(const PromptArgs& a, int s, bool check) {
+  SeqSpan x{0, 0, 0, 0, 0};
+  if (s >= a.nseq) return x;
+  const int q0 = __ldg(a.cu_q + s), q1 = __ldg(a.cu_q + s + 1);
+  const int k0 = __ldg(a.cu_k + s), k1 = __ldg(a.cu_k + s + 1);
+  if (q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 && k1 <= a.total_k &&
+      q1 - q0 <= a.max_q && k1 - k0 <= a.max_k)
+    return SeqSpan{q0, q1 - q0, k0, k1 - k0, (q1 - q0 + a.tpt - 1) / a.tpt};
+  if (check) report(a.err, KVQ_DEVERR_INDEX);
+  return x;
+}
+
+__device__ __forceinline__ Unit unit_of(const SeqSpan& x, int src, int tile, int h) {
+  Unit r;
+  r.q0 = __shfl_sync(kFullMask, x.q0, src);
+  r.lq = __shfl_sync(kFullMask, x.lq, src);
+  r.k0 = __shfl_sync(kFullMask, x.k0, src);
+  r.lk = __shfl_sync(kFullMask, x.lk, src);
+  r.tile = tile;
+  r.h = h;
+  r.found = true;
+  return r;
+}
+
+// The unit of linear index u, found by a whole warp.  Late tiles have the most keys, and the CTAs
+// that start last should have the least to do: with up to 32 sequences the tiles of all of them go
+// from the highest number to the lowest; with more, sequences go in order, the tiles of each from
+// the last to the first.  For each tile, its KV heads.  With `check` set every sequence is looked
+// at and reported.  A call's units fit 31 bits.
 __device__ __forceinline__ Unit find_unit(const PromptArgs& a, int u, bool check) {
   const int lane = threadIdx.x & 31;
+  const uint32_t at = static_cast<uint32_t>(u);
+  if (a.nseq <= 32) {
+    const SeqSpan x = span_of(a, lane, check);
+    // units of tiles numbered t and more
+    auto from = [&](int t) {
+      return __reduce_add_sync(kFullMask, static_cast<uint32_t>(max(0, x.tiles - t))) * a.H;
+    };
+    Unit none;
+    none.found = false;
+    if (at >= from(0)) return none;
+    int lo = 0, hi = __reduce_max_sync(kFullMask, x.tiles);   // from(lo) > at, from(hi) <= at
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (from(mid) > at) lo = mid;
+      else hi = mid;
+    }
+    const uint32_t rem = at - from(lo + 1), k = rem / a.H;
+    const unsigned with = __ballot_sync(kFullMask, x.tiles > lo);
+    const unsigned hit = __ballot_sync(
+        kFullMask, x.tiles > lo && __popc(with & ((1u << lane) - 1)) == static_cast<int>(k));
+    return unit_of(x, __ffs(hit) - 1, lo, static_cast<int>(rem - k * a.H));
+  }
   Unit r;
   r.found = false;
-  uint32_t before = 0;   // a call's units fit 31 bits
+  uint32_t before = 0;
   for (int base = 0; base < a.nseq; base += 32) {
-    const int s = base + lane;
-    int q0 = 0, q1 = 0, k0 = 0, k1 = 0, tiles = 0;
-    if (s < a.nseq) {
-      q0 = __ldg(a.cu_q + s);
-      q1 = __ldg(a.cu_q + s + 1);
-      k0 = __ldg(a.cu_k + s);
-      k1 = __ldg(a.cu_k + s + 1);
-      const bool ok = q0 >= 0 && q1 >= q0 && q1 <= a.total_q && k0 >= 0 && k1 >= k0 &&
-                      k1 <= a.total_k && q1 - q0 <= a.max_q && k1 - k0 <= a.max_k;
-      if (ok) tiles = (q1 - q0 + a.tpt - 1) / a.tpt;
-      else if (check) report(a.err, KVQ_DEVERR_INDEX);
-    }
-    const uint32_t mine = static_cast<uint32_t>(tiles) * a.H;
+    const SeqSpan x = span_of(a, base + lane, check);
+    const uint32_t mine = static_cast<uint32_t>(x.tiles) * a.H;
     uint32_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(kFullMask, incl, o);
-      if (lane >= o) incl += x;
+      const uint32_t y = __shfl_up_sync(kFullMask, incl, o);
+      if (lane >= o) incl += y;
     }
-    const uint32_t start = before + incl - mine, at = static_cast<uint32_t>(u);
+    const uint32_t start = before + incl - mine;
     const unsigned hit = __ballot_sync(kFullMask, at >= start && at - start < mine);
     if (hit && !r.found) {
       const int src = __ffs(hit) - 1;
       const uint32_t rem = __shfl_sync(kFullMask, at - start, src);
-      const uint32_t t = __shfl_sync(kFullMask, tiles, src);
-      r.q0 = __shfl_sync(kFullMask, q0, src);
-      r.lq = __shfl_sync(kFullMask, q1, src) - r.q0;
-      r.k0 = __shfl_sync(kFullMask, k0, src);
-      r.lk = __shfl_sync(kFullMask, k1, src) - r.k0;
       const uint32_t back = rem / a.H;
-      r.h = static_cast<int>(rem - back * a.H);
-      r.tile = static_cast<int>(t - 1 - back);
-      r.found = true;
+      r = unit_of(x, src, __shfl_sync(kFullMask, x.tiles, src) - 1 - static_cast<int>(back),
+                  static_cast<int>(rem - back * a.H));
       if (!check) return r;
     }
     before += __shfl_sync(kFullMask, incl, 31);
@@ -168,33 +203,32 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
   return __all_sync(kFullMask, tc5::wait(bar, parity, gave_up));
 }
 
-// A V slot before its product, in a tile where some row's view ends: key t0 + i of row i of the
-// slot.  Keys no row sees are zeroed; non-finite values that only some rows see are zeroed and
-// noted in *flag.
+// A V slot before its product, in a tile where some row's view ends: row i of the slot is key
+// t0 + i.  Keys no row sees are zeroed; non-finite values that only some rows see are zeroed and
+// noted in *flag.  (A row's 128-byte pieces may be taken in any order: the swizzle stays inside.)
 template <bool BF, int D, int VR>
 __device__ __forceinline__ void clean_v(unsigned char* slot, int t0, int lim_min, int lim_max,
                                         int* flag) {
+  constexpr int P = D / 8;   // 16-byte pieces of a key
+  const int a = max(0, lim_min - t0), b = min(VR, max(a, lim_max - t0));
+  auto at = [&](int row, int c) {
+    return reinterpret_cast<uint4*>(slot + (c >> 3) * VR * 128 + row * 128 + (c & 7) * 16);
+  };
   bool found = false;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < VR * D / 8; i += kSoftmaxThreads) {
-    const int t = t0 + ((i >> 3) % VR);
-    if (t < lim_min) continue;
-    uint4* p = reinterpret_cast<uint4*>(slot + i * 16);
-    if (t >= lim_max) {
-      *p = make_uint4(0, 0, 0, 0);
-    } else {
-      uint4 w = *p;
-      if (nonfinite2<BF>(w.x) || nonfinite2<BF>(w.y) || nonfinite2<BF>(w.z) ||
-          nonfinite2<BF>(w.w)) {
-        w.x = finite2<BF>(w.x);
-        w.y = finite2<BF>(w.y);
-        w.z = finite2<BF>(w.z);
-        w.w = finite2<BF>(w.w);
-        *p = w;
-        found = true;
-      }
+  for (int i = threadIdx.x; i < (b - a) * P; i += kSoftmaxThreads) {
+    uint4* p = at(a + i / P, i % P);
+    uint4 w = *p;
+    if (nonfinite2<BF>(w.x) || nonfinite2<BF>(w.y) || nonfinite2<BF>(w.z) || nonfinite2<BF>(w.w)) {
+      w.x = finite2<BF>(w.x);
+      w.y = finite2<BF>(w.y);
+      w.z = finite2<BF>(w.z);
+      w.w = finite2<BF>(w.w);
+      *p = w;
+      found = true;
     }
   }
+  for (int i = threadIdx.x; i < (VR - b) * P; i += kSoftmaxThreads)
+    *at(b + i / P, i % P) = make_uint4(0, 0, 0, 0);
   if (found) *flag = 1;
 }
 
