@@ -11,9 +11,9 @@
 // TMEM is full: O 256 columns, two score buffers of 64, Q 128.  With Q in TMEM the first product
 // reads only K_hat from shared memory, whose bandwidth is the scarcest after the codes' arrival.
 //
-// Roles of the 26 warps of a persistent CTA (one per SM): 8 softmax, 1 issues the products, 1
-// brings codes and scales (16-token groups of a page) into a ring deep enough to cover the memory
-// latency, 16 unpack.
+// Roles of the 19 warps of a persistent CTA (one per SM): 8 softmax, 1 issues the products, 2
+// bring codes and scales of K and of V (16-token groups of a page) into rings deep enough to cover
+// the memory latency, 8 unpack.
 //
 // Work: the tiles of all (layer, sequence, KV head, row tile) units in one line are dealt to the
 // CTAs in equal contiguous shares, whatever the sequences' lengths (which only the device knows).
@@ -43,7 +43,7 @@ constexpr int kD = 256;
 constexpr int kRows = 128;
 constexpr int kTile = 64;             // tokens per tile
 constexpr int kSoftmaxWarps = 8;      // warps 0-7: two threads per row, half of the columns each
-constexpr int kMmaWarp = 8, kCopyWarp = 9, kUnpackWarp0 = 10, kUnpackWarps = 8;
+constexpr int kMmaWarp = 8, kCopyWarp = 9, kUnpackWarp0 = 11, kUnpackWarps = 8;   // copies: K 9, V 10
 constexpr int kThreads = (kUnpackWarp0 + kUnpackWarps) * 32;
 constexpr int kRec = (kD + 2) * kRows;   // a partial record: O [256 / 4][128 rows][4], then m and l [128]
 constexpr int kShortTiles = 8;        // caches of at most so many tiles are not cut
@@ -87,15 +87,16 @@ struct TreeArgs {
 template <int BITS>
 struct Lay {
   static constexpr int kPd = kD * BITS / 8;
-  static constexpr int kRaw = 2 * kTile * kPd + 4 * kTile;   // K codes, V codes, K and V scales
+  static constexpr int kRaw = kTile * kPd + 2 * kTile;   // codes and scales of K or V
   static constexpr int kRaws = BITS == 8 ? 3 : BITS == 6 ? 4 : 6;
   static constexpr int kK = 0, kV = 2 * kStage, kRawAt = 4 * kStage;
-  static constexpr int kBars = kRawAt + kRaws * kRaw;
-  static constexpr int kNumBars = 2 * kRaws + 4 * 2 + 3 * 2 + 2;
+  static constexpr int kBars = kRawAt + 2 * kRaws * kRaw;
+  static constexpr int kNumBars = 4 * kRaws + 4 * 2 + 3 * 2 + 2;
   static constexpr int kTail = kBars + kNumBars * 8;         // then: TMEM address, flags, meta,
   static constexpr int kParents = kTail + 16 + kMeta * 4;    // and the parents
   static constexpr int kHalves = kParents + KVQ_MAX_NODES;       // and the exchange [2][128]
-  static constexpr int kTotal = kHalves + 2 * kRows * 4;
+  static constexpr int kConst = kHalves + 2 * kRows * 4;          // and the unpacking's constants
+  static constexpr int kTotal = kConst + 16;
   static_assert(kTotal <= 232448, "shared memory");
 };
 
@@ -245,6 +246,28 @@ __device__ __forceinline__ bool next_segment(const TreeArgs& a, Walk& w, Segment
   return g.u.s >= 0;
 }
 
+// The constants of the unpacking, read from shared memory into registers once per warp: spelt out
+// in the code, the compiler sets them anew at most uses (an instruction takes one immediate), which
+// was a quarter of all instructions.
+template <int BITS> __device__ __forceinline__ constexpr uint32_t unpack_constant(int i) {
+  if (BITS == 8) return i == 0 ? 0x80808080u : i == 1 ? 0x64646464u : kHm1152;
+  if (BITS == 6)
+    return i == 0 ? 0x03F0003Fu : i == 1 ? 0x64006400u : i == 2 ? 0x2C003C00u : 0xD600E420u;
+  return i == 0 ? 0x000F000Fu : i == 1 ? 0x64006400u : i == 2 ? kHm1032 : kHm72;
+}
+
+__device__ __forceinline__ uint32_t hadd2u(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// (x & m) | o in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(m), "r"(o));
+  return r;
+}
+
 // 16 codes of a row (2 * BITS bytes in shared memory), and their product with the row's scale as
 // two 16-byte pieces in the stored order of channels.
 template <int BITS> struct Codes;
@@ -252,13 +275,13 @@ template <int BITS> struct Codes;
 template <> struct Codes<8> {
   uint4 v;
   __device__ __forceinline__ void load(const unsigned char* p) { v = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void unpack(uint32_t scale2, uint32_t o[8]) const {
+  __device__ __forceinline__ void unpack(uint32_t scale2, const uint32_t k[4], uint32_t o[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t u = w[i] ^ 0x80808080u;   // c + 128
-      o[2 * i] = hmul2u(hfma2u(prmt(u, 0x64646464u, 0x4140), kH1, kHm1152), scale2);
-      o[2 * i + 1] = hmul2u(hfma2u(prmt(u, 0x64646464u, 0x4342), kH1, kHm1152), scale2);
+      const uint32_t u = w[i] ^ k[0];   // c + 128
+      o[2 * i] = hmul2u(hadd2u(prmt(u, k[1], 0x4140), k[2]), scale2);
+      o[2 * i + 1] = hmul2u(hadd2u(prmt(u, k[1], 0x4342), k[2]), scale2);
     }
   }
 };
@@ -271,17 +294,16 @@ template <> struct Codes<6> {
     w1 = x[1];
     w2 = x[2];
   }
-  __device__ __forceinline__ void unpack(uint32_t scale2, uint32_t o[8]) const {
+  __device__ __forceinline__ void unpack(uint32_t scale2, const uint32_t k[4], uint32_t o[8]) const {
     // per group of 4: low half bytes 0-1 (u0 at bit 0, u1 at 6), high half bytes 1-2 (u2 at 4,
-    // u3 at 10): the mask leaves (u0, 16 u2), and after a shift by 6 (u1, 16 u3)
+    // u3 at 10): the mask leaves (u0, 16 u2), and after a shift by 6 (u1, 16 u3); 1 and 1/16 and
+    // the offsets 1056 and 96 make them codes
     const uint32_t x[4] = {prmt(w0, w0, 0x2110), prmt(w0, w1, 0x5443), prmt(w1, w2, 0x4332),
                            prmt(w2, w2, 0x3221)};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t a = (x[i] & 0x03F0003Fu) | 0x64006400u;
-      const uint32_t b = ((x[i] >> 6) & 0x03F0003Fu) | 0x64006400u;
-      o[2 * i] = hmul2u(hfma2u(a, 0x2C003C00u, 0xD600E420u), scale2);
-      o[2 * i + 1] = hmul2u(hfma2u(b, 0x2C003C00u, 0xD600E420u), scale2);
+      o[2 * i] = hmul2u(hfma2u(and_or(x[i], k[0], k[1]), k[2], k[3]), scale2);
+      o[2 * i + 1] = hmul2u(hfma2u(and_or(x[i] >> 6, k[0], k[1]), k[2], k[3]), scale2);
     }
   }
 };
@@ -289,15 +311,15 @@ template <> struct Codes<6> {
 template <> struct Codes<4> {
   uint2 v;
   __device__ __forceinline__ void load(const unsigned char* p) { v = *reinterpret_cast<const uint2*>(p); }
-  __device__ __forceinline__ void unpack(uint32_t scale2, uint32_t o[8]) const {
-    const uint32_t w[2] = {v.x, v.y};
+  __device__ __forceinline__ void unpack(uint32_t scale2, const uint32_t k[4], uint32_t o[8]) const {
+    const uint32_t w[2] = {v.x, v.y}, hi = k[0] << 4;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t y = w[i] >> 8;
-      o[4 * i] = hmul2u(hfma2u((w[i] & 0x000F000Fu) | 0x64006400u, kH1, kHm1032), scale2);
-      o[4 * i + 1] = hmul2u(hfma2u((w[i] & 0x00F000F0u) | 0x64006400u, kH16th, kHm72), scale2);
-      o[4 * i + 2] = hmul2u(hfma2u((y & 0x000F000Fu) | 0x64006400u, kH1, kHm1032), scale2);
-      o[4 * i + 3] = hmul2u(hfma2u((y & 0x00F000F0u) | 0x64006400u, kH16th, kHm72), scale2);
+      o[4 * i] = hmul2u(hadd2u(and_or(w[i], k[0], k[1]), k[2]), scale2);
+      o[4 * i + 1] = hmul2u(hfma2u(and_or(w[i], hi, k[1]), kH16th, k[3]), scale2);
+      o[4 * i + 2] = hmul2u(hadd2u(and_or(y, k[0], k[1]), k[2]), scale2);
+      o[4 * i + 3] = hmul2u(hfma2u(and_or(y, hi, k[1]), kH16th, k[3]), scale2);
     }
   }
 };
@@ -332,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   constexpr int R = L::kRaws;
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
-  uint64_t *rawfull = bars, *rawempty = bars + R, *kfull = bars + 2 * R, *kempty = kfull + 2,
+  uint64_t *rawfull = bars, *rawempty = bars + 2 * R, *kfull = bars + 4 * R, *kempty = kfull + 2,
            *vfull = kempty + 2, *vempty = vfull + 2, *sfull = vempty + 2, *pready = sfull + 2,
            *odone = pready + 2, *qready = odone + 2, *drain = qready + 1;
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(sm + L::kTail);
@@ -359,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   if (w.at >= w.end) return;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < R; ++i) { mbar_init(rawfull + i, 1); mbar_init(rawempty + i, kUnpackWarps); }
+    for (int i = 0; i < 2 * R; ++i) { mbar_init(rawfull + i, 1); mbar_init(rawempty + i, kUnpackWarps / 2); }
     for (int i = 0; i < 2; ++i) {
       mbar_init(kfull + i, kUnpackWarps / 2);
       mbar_init(kempty + i, 1);
@@ -374,6 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     tc5::fence_barrier_init();
     flags[0] = 0;
     flags[1] = 0;
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<uint32_t*>(sm + L::kConst)[i] = unpack_constant<BITS>(i);
   }
   if (warp == kMmaWarp) tc5::tmem_alloc(tmem_ptr, kCols);
   tc5::fence_before();
@@ -384,14 +408,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
   int it = 0;        // tiles done by this CTA
   bool ok = true;
 
-  if (warp == kCopyWarp) {
+  if (warp == kCopyWarp || warp == kCopyWarp + 1) {
     // ------------------------------------------------------------------------- copies
-    // Eight tiles at a time: lane i looks up the page of 16-token group i, then all lanes read
-    // those tiles' scales (lane = K or V, four tokens; scales of tokens that are not there become
-    // 0, so that their rows unpack to zeros).  The next eight, of the next segment too, are looked
-    // up while the tiles of the present ones go out, one bulk copy per group for each of K and V
-    // codes.
-    const int kind = lane >> 4, sub = lane & 15;
+    // One warp for K and one for V, each with a ring of its own: the keys are used about two tiles
+    // before the values, and would wait for them in a common one.  Eight tiles at a time: lane i
+    // looks up the page of 16-token group i, then all lanes read those tiles' scales (two tokens
+    // each; scales of tokens that are not there become 0, so that their rows unpack to zeros).
+    // The next eight, of the next segment too, are looked up while the tiles of the present ones
+    // go out, one bulk copy of codes per group.
+    const int kind = warp - kCopyWarp;
+    uint64_t *full = rawfull + kind * R, *empty = rawempty + kind * R;
+    unsigned char* ring = sm + L::kRawAt + kind * R * L::kRaw;
     struct Batch {
       int first, total, n, l, h, s;   // first token, end of the sequence, tiles, unit
     };
@@ -420,26 +447,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     auto row_of = [&](const Batch& x, int page) -> uint32_t {
       if (page == -2) return kNoRow;
       if (page < 0 || page >= a.L[x.l].k_pages || page >= a.L[x.l].v_pages) {
-        report(a.err, KVQ_DEVERR_PAGE_RANGE);
+        if (kind == 0) report(a.err, KVQ_DEVERR_PAGE_RANGE);
         return kNoRow;
       }
       const int tg = x.first + lane * 16;
       return (static_cast<uint32_t>(page) * a.H + x.h) * a.ps + tg % a.ps;
     };
-    auto load_scales = [&](const Batch& x, uint32_t rows, uint2 v[8]) {
+    auto load_scales = [&](const Batch& x, uint32_t rows, uint32_t v[8]) {
       const uint16_t* scales = kind ? a.L[x.l].vs : a.L[x.l].ks;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t r = __shfl_sync(kFullMask, rows, j * 4 + (sub >> 2));
-        v[j] = r != kNoRow ? ld_nc_v2(scales + r + (sub & 3) * 4) : make_uint2(0, 0);
+        const uint32_t r = __shfl_sync(kFullMask, rows, j * 4 + (lane >> 3));
+        v[j] = r != kNoRow ? ld_nc_u32(scales + r + (lane & 7) * 2) : 0u;
       }
     };
     Batch cur = next_batch();
     uint32_t rows = row_of(cur, page_of(cur));
-    uint2 x[8], nx[8];
+    uint32_t x[8], nx[8];
     load_scales(cur, rows, x);
     while (ok && cur.n > 0) {
-      const uint8_t *kc = a.L[cur.l].kc, *vc = a.L[cur.l].vc;
+      const uint8_t* codes = kind ? a.L[cur.l].vc : a.L[cur.l].kc;
       Batch nxt = next_batch();
       const int page = page_of(nxt);
       uint32_t next_rows = kNoRow;
@@ -451,17 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
         if (!ok || j >= cur.n) continue;
         const int st = it % R;
-        if (it >= R) ok = warp_wait(rawempty + st, (it / R + 1) & 1, flags);
+        if (it >= R) ok = warp_wait(empty + st, (it / R + 1) & 1, flags);
         if (!ok) continue;
-        unsigned char* dst = sm + L::kRawAt + st * L::kRaw;
-        const int left = cur.total - (cur.first + j * kTile + sub * 4);   // tokens still there
-        if (left < 4) {
-          if (left < 1) x[j].x &= 0xffff0000u;
-          if (left < 2) x[j].x &= 0x0000ffffu;
-          if (left < 3) x[j].y &= 0xffff0000u;
-          x[j].y &= 0x0000ffffu;
-        }
-        *reinterpret_cast<uint2*>(dst + 2 * kTile * L::kPd + kind * 2 * kTile + sub * 8) = x[j];
+        unsigned char* dst = ring + st * L::kRaw;
+        const int left = cur.total - (cur.first + j * kTile + lane * 2);   // tokens still there
+        if (left < 2) x[j] &= left < 1 ? 0u : 0x0000ffffu;
+        *reinterpret_cast<uint32_t*>(dst + kTile * L::kPd + lane * 4) = x[j];
         uint32_t r[4];
         unsigned have = 0;
 #pragma unroll
@@ -471,15 +493,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         }
         __syncwarp();
         if (tc5::elect_one()) {   // copies by several lanes at once take 100 cycles each
-          meta[it % kMeta] = static_cast<int>(have);
-          mbar_expect_tx(rawfull + st, __popc(have) * (2 * 16 * L::kPd));
+          if (kind == 0) meta[it % kMeta] = static_cast<int>(have);
+          mbar_expect_tx(full + st, __popc(have) * (16 * L::kPd));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (r[i] == kNoRow) continue;
-            const uint64_t at = static_cast<uint64_t>(r[i]) * L::kPd;
-            bulk_g2s(dst + i * 16 * L::kPd, kc + at, 16 * L::kPd, rawfull + st);
-            bulk_g2s(dst + (kTile + i * 16) * L::kPd, vc + at, 16 * L::kPd, rawfull + st);
-          }
+          for (int i = 0; i < 4; ++i)
+            if (r[i] != kNoRow)
+              bulk_g2s(dst + i * 16 * L::kPd, codes + static_cast<uint64_t>(r[i]) * L::kPd,
+                       16 * L::kPd, full + st);
         }
         __syncwarp();
         ++it;
@@ -490,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       for (int j = 0; j < 8; ++j) x[j] = nx[j];
     }
     if (!ok) {   // wait for the copies in flight
-      for (int i = max(0, it - R); i < it; ++i) mbar_wait_bounded(rawfull + i % R, (i / R) & 1);
+      for (int i = max(0, it - R); i < it; ++i) mbar_wait_bounded(full + i % R, (i / R) & 1);
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products (one thread)
@@ -557,18 +577,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     const int kv = (warp - kUnpackWarp0) / W, uw = (warp - kUnpackWarp0) % W;
     const int q = lane >> 3, rr = (lane >> 2) & 1, u = lane & 3;
     const int src = (q * 4 + u) * 2 * BITS;
+    uint32_t k[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      k[i] = reinterpret_cast<const volatile uint32_t*>(sm + L::kConst)[i];
     uint64_t *full = kv ? vfull : kfull, *empty = kv ? vempty : kempty;
+    uint64_t *rfull = rawfull + kv * R, *rempty = rawempty + kv * R;
+    const unsigned char* ring = sm + L::kRawAt + kv * R * L::kRaw;
     unsigned char* stages = sm + (kv ? L::kV : L::kK) + q * kTile * 128;
     constexpr int S = kTile / 2 / W;   // steps
     while (ok && next_segment(a, w, g)) {
       const int len = g.u.q.len;
       for (int j = 0; j < g.count; ++j, ++it) {
         const int st = it % R, t0 = (g.u.tile + j) * kTile;
-        ok = warp_wait(rawfull + st, (it / R) & 1, flags);
+        ok = warp_wait(rfull + st, (it / R) & 1, flags);
         if (!ok) break;
-        const unsigned char* raw = sm + L::kRawAt + st * L::kRaw + kv * kTile * L::kPd;
-        const uint16_t* sc = reinterpret_cast<const uint16_t*>(
-            sm + L::kRawAt + st * L::kRaw + 2 * kTile * L::kPd + kv * 2 * kTile);
+        const unsigned char* raw = ring + st * L::kRaw;
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(raw + kTile * L::kPd);
         Codes<BITS> c[S];
         uint32_t s1[S];
 #pragma unroll
@@ -578,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           s1[i] = sc[row];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(rawempty + st);   // all read: the next copies may come
+        if (lane == 0) mbar_arrive(rempty + st);   // all read: the next copies may come
         if (it >= 2) ok = warp_wait(empty + (it & 1), (it / 2 + 1) & 1, flags);
         if (!ok) break;
         unsigned char* dst = stages + (it & 1) * kStage;
@@ -593,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
           for (int i = 0; i < S; ++i) {
             uint32_t o[8];
-            c[i].unpack(s1[i] | (s1[i] << 16), o);
+            c[i].unpack(s1[i] | (s1[i] << 16), k, o);
             store((i * W + uw) * 2 + rr, o);
           }
         } else {   // drafts among the values: 0 * inf must not reach the rows that do not see them
@@ -601,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           for (int i = 0; i < S; ++i) {
             const int row = (i * W + uw) * 2 + rr;
             uint32_t o[8];
-            c[i].unpack(s1[i] | (s1[i] << 16), o);
+            c[i].unpack(s1[i] | (s1[i] << 16), k, o);
             if (t0 + row >= len) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
