@@ -799,13 +799,17 @@ def _raw_stream(stream, dev: int) -> int:
 
 def _pool_structs(pools: Sequence[Pool], dev: int) -> ctypes.Array:
     """The pools as an array of kvq_pool (five 64-bit words each)."""
-    words = []
-    for p in pools:
-        if p.codes.get_device() != dev or p.scales.get_device() != dev:
-            raise ValueError("the pools are not on the current device")
-        words += (p.bits & 0xffffffff | p.num_heads << 32, p.head_dim & 0xffffffff | p.page_size << 32,
-                  p.codes.shape[0], p.codes.data_ptr(), p.scales.data_ptr())
-    return (kvq_pool * len(pools)).from_buffer(array.array("Q", words))
+    words = array.array("Q")
+    try:
+        for p in pools:
+            c, s = p.codes, p.scales
+            if c.get_device() != dev or s.get_device() != dev:
+                raise ValueError("the pools are not on the current device")
+            words.extend((p.bits | p.num_heads << 32, p.head_dim | p.page_size << 32, c.size(0),
+                          c.data_ptr(), s.data_ptr()))
+    except OverflowError:   # a negative field: left to the library's checks
+        return _pool_array(pools)
+    return (kvq_pool * len(pools)).from_buffer(words)
 
 
 def kvq_rope_phases(inv_freq, device="cuda") -> torch.Tensor:

@@ -81,6 +81,33 @@ def test_group_sizes(kvq, cuda_dev, G):
     _check(kvq, cuda_dev, "f16", [3, 70], [3, 150], G, 1, 64, seed=G)
 
 
+def test_more_sequences_than_a_warp_has_lanes(kvq, cuda_dev):
+    """33 sequences and more are laid out in another order; empty ones among them."""
+    r = np.random.default_rng(1)
+    for n, top, past, D in ((33, 60, 0, 64), (70, 9, 300, 128), (100, 3, 2, 256)):
+        new = [int(x) for x in r.integers(0, top, n)]
+        keys = [a + int(x) for a, x in zip(new, r.integers(0, past + 1, n))]
+        _check(kvq, cuda_dev, "f16", new, keys, 4, 2, D, seed=n, tail=2)
+
+
+def test_tiles_that_end_at_the_view_of_their_first_row(kvq, cuda_dev):
+    """Key counts around multiples of the key tile, one row and several."""
+    for D, nb in ((256, 128), (128, 64), (64, 64)):
+        for keys in (nb - 1, nb, nb + 1, 2 * nb, 5 * nb, 5 * nb + 1):
+            _check(kvq, cuda_dev, "f16", [1, 3], [keys, keys], 6, 1, D, seed=keys)
+
+
+def test_a_non_finite_query_spoils_its_own_row_only(kvq, cuda_dev):
+    q, k, v = _inputs(cuda_dev, "f16", [90], [90], 6, 1, 128, 21)
+    clean, _, _ = _call(kvq, q, k, v, [90], [90], 0.088)
+    q[40, 2, 5], q[41, 3, 0] = float("nan"), float("inf")
+    out, _, err = _call(kvq, q, k, v, [90], [90], 0.088)
+    assert err == 0 and torch.isnan(out[40, 2]).all() and torch.isnan(out[41, 3]).any()
+    keep = torch.ones((90, 6), dtype=torch.bool)
+    keep[40, 2] = keep[41, 3] = False
+    assert torch.equal(out[keep], clean[keep])
+
+
 def test_views_of_a_fused_projection(kvq, cuda_dev):
     for D in (64, 256):
         _check(kvq, cuda_dev, "f16", [100, 33], [100, 33], 6, 2, D, fused=True)

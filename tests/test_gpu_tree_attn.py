@@ -106,6 +106,38 @@ def test_layers_in_one_call(kvq, cuda_dev):
     _check(kvq, cuda_dev, 4, 2, 6, [77, 200], [5, 12], layers=3, seed=3)
 
 
+def test_many_sequences_and_units(kvq, cuda_dev):
+    """More units than SMs, with short caches (whole units per CTA) and longer ones (several
+    segments, cut units in the middle of a share), empty trees among them."""
+    r = np.random.default_rng(3)
+    for n, top, most in ((90, 200, 4), (70, 1400, 3)):
+        lens = [int(x) for x in r.integers(0, top, n)]
+        nodes = [int(x) for x in r.integers(0, most, n)]
+        _check(kvq, cuda_dev, 6, 4, 2, lens, nodes, seed=n, tail=1)
+
+
+def test_layers_and_cut_units(kvq, cuda_dev):
+    _check(kvq, cuda_dev, 8, 2, 6, [700, 1500, 30], [30, 2, 64], layers=2, seed=5)
+
+
+def test_scores_that_rise_along_the_cache(kvq, cuda_dev):
+    """The running maximum moves in every tile."""
+    n, nodes = 900, 5
+    c = Cache(kvq, cuda_dev, 8, 1, 16, [n], [nodes], seed=11)
+    t = np.arange(n + nodes, dtype=np.float64)
+    k = np.repeat((t / n * 40)[:, None, None], D, 2).astype(np.float16)
+    kvq.kvq_quant_pack_paged(c.kp, [dev_tensor(k, cuda_dev)], c.pt, i32([0, n + nodes], cuda_dev),
+                             i32([0], cuda_dev))
+    s, codes = osym.quantize_rows(k, 8)
+    c.k_hat[0] = osym.dequantize_rows(codes, s)
+    q_np = np.full((1, nodes, 6, D), 0.25, dtype=np.float16)
+    parents = [_parents(nodes, 1)]
+    out, err = _call(kvq, cuda_dev, c, dev_tensor(q_np, cuda_dev), parents)
+    assert err == 0
+    ref, size, span = _reference(c, q_np[0], parents)
+    assert_rows_close(out[0].double().cpu().numpy(), ref, size, span, "f16")
+
+
 def test_a_chain_equals_single_decode_steps(kvq, cuda_dev):
     """Node i of a chain attends as kvq_decode_attn does over the tokens up to it."""
     c, _, q_np, out = _check(kvq, cuda_dev, 6, 2, 6, [333, 70], [9, 9], chain=True, seed=4)
