@@ -560,7 +560,8 @@ KVQ_API kvq_status kvq_rope_phases(const double* inv_freq, int n, uint64_t* phas
  * and then its first rotary_dim values are rotated in pairs (a, b), pair i by the angle
  * positions[t] * inv_freq[i]:  a' = a cos - b sin,  b' = b cos + a sin, with (a, b) =
  * (y_i, y_{i + rotary_dim / 2}), or (y_{2i}, y_{2i+1}) if interleaved.  Computed in float32 from
- * the inputs, rounded once to the output type.
+ * the inputs, rounded once to the output type.  A row whose sum of squares exceeds float32 (bf16
+ * values of 1e19 and more) becomes 0, a row of zeros with eps 0 NaN.
  * q, k           device, `dtype`, [num_tokens][heads][D], a token's heads contiguous, tokens
  *                q_stride / k_stride elements apart (a multiple of 8, >= heads * D): views into a
  *                fused projection's output are fine.  num_tokens may be 0.
@@ -612,7 +613,8 @@ KVQ_API kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64_t 
  * head_dim 64, 128 or 256; any Hq that is a multiple of H, at most 128 query heads per KV head.
  * Two calls with the same arguments give the same bits.
  * Errors: KVQ_ERR_SHAPE (dtype, heads, head_dim, strides), KVQ_ERR_NULL, KVQ_ERR_ALIGN,
- * KVQ_ERR_RANGE (counts; softmax_scale not finite or <= 0), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
+ * KVQ_ERR_RANGE (counts, total_k above 2^31 - 129, more than 2^31 - 1 tiles of 128 rows;
+ * softmax_scale not in (0, 2.3e38]), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
  */
 KVQ_API size_t kvq_prompt_attn_workspace(int nseq, int total_q, int num_q_heads, int num_kv_heads,
                                          int head_dim, int max_q, int max_k);
@@ -653,9 +655,11 @@ KVQ_API kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_t q
  * workspace  kvq_tree_attn_workspace(...) bytes, 16-byte aligned, no initialisation needed; two
  *            calls that may overlap need one each.
  * Values of drafts that a node does not see (infinities and NaN too) do not reach it.
- * head_dim 256; page_size a multiple of 16; at most 16 query heads per KV head.
- * Errors: KVQ_ERR_SHAPE, KVQ_ERR_BITS, KVQ_ERR_NULL, KVQ_ERR_ALIGN, KVQ_ERR_RANGE,
- * KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
+ * head_dim 256; page_size a multiple of 16; at most 16 query heads per KV head.  One call's upper
+ * bounds may make 2^30 tiles of 64 tokens at most (layers x KV heads x tiles of 128 rows x
+ * max_seq_len / 64), and max_seq_len may be 2^31 - 65.
+ * Errors: KVQ_ERR_SHAPE, KVQ_ERR_BITS, KVQ_ERR_NULL, KVQ_ERR_ALIGN, KVQ_ERR_RANGE (also
+ * softmax_scale not in (0, 2.3e38]), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
  */
 KVQ_API size_t kvq_tree_attn_workspace(int n_layers, int nseq, int total_nodes, int num_kv_heads,
                                        int num_q_heads, int head_dim, int max_nodes,

@@ -46,13 +46,14 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kSoftmaxThreads = 128;
 constexpr int kThreads = 192;
+constexpr int kScores = 2;   // score buffers
 
 // NB: keys per tile.  KD: channels of a K slot (NB rows).  VR: keys of a V slot (D channels).
-// NS: score buffers.  kSlots: ring slots.  kCtas: resident CTAs per SM.
+// kSlots: ring slots.  kCtas: resident CTAs per SM.
 template <int D> struct Cfg;
-template <> struct Cfg<256> { static constexpr int NB = 128, KD = 128, VR = 64, NS = 2, kSlots = 5, kCtas = 1; };
-template <> struct Cfg<128> { static constexpr int NB = 64, KD = 128, VR = 64, NS = 2, kSlots = 5, kCtas = 2; };
-template <> struct Cfg<64> { static constexpr int NB = 64, KD = 64, VR = 64, NS = 2, kSlots = 8, kCtas = 2; };
+template <> struct Cfg<256> { static constexpr int NB = 128, KD = 128, VR = 64, kSlots = 5, kCtas = 1; };
+template <> struct Cfg<128> { static constexpr int NB = 64, KD = 128, VR = 64, kSlots = 5, kCtas = 2; };
+template <> struct Cfg<64> { static constexpr int NB = 64, KD = 64, VR = 64, kSlots = 8, kCtas = 2; };
 
 template <int D>
 struct Lay {
@@ -62,10 +63,10 @@ struct Lay {
   static_assert(kSlot == C::VR * D * 2, "K and V slots are alike");
   static constexpr int kRing = kQ;
   static constexpr int kBars = kRing + C::kSlots * kSlot;
-  static constexpr int kNumBars = 2 * C::kSlots + 3 + 2 * C::NS;
+  static constexpr int kNumBars = 2 * C::kSlots + 3 + 2 * kScores;
   static constexpr int kTotal = kBars + kNumBars * 8 + 16;
   static constexpr int kCols = 512 / C::kCtas;
-  static_assert(D + C::NS * C::NB <= kCols, "TMEM");
+  static_assert(D + kScores * C::NB <= kCols, "TMEM");
   static constexpr int nk = D / C::KD, nv = C::NB / C::VR;
 };
 
@@ -238,11 +239,11 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using C = Cfg<D>;
   using L = Lay<D>;
-  constexpr int NB = C::NB, NS = C::NS, SL = C::kSlots;
+  constexpr int NB = C::NB, SL = C::kSlots;
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
   uint64_t *full = bars, *empty = bars + SL, *qfull = bars + 2 * SL, *odone = qfull + 1,
-           *sfull = odone + 2, *pready = sfull + NS;
+           *sfull = odone + 2, *pready = sfull + kScores;
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_ptr + 1);   // [0] gave up, [1] V
 
@@ -261,7 +262,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     mbar_init(qfull, 1);
     mbar_init(odone, 1);
     mbar_init(odone + 1, 1);
-    for (int i = 0; i < NS; ++i) { mbar_init(sfull + i, 1); mbar_init(pready + i, kSoftmaxThreads / 32); }
+    for (int i = 0; i < kScores; ++i) { mbar_init(sfull + i, 1); mbar_init(pready + i, kSoftmaxThreads / 32); }
     tc5::fence_barrier_init();
     flags[0] = 0;
     flags[1] = 0;
@@ -313,13 +314,8 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       };
       load_k(0);
       for (int j = 0; j < nt && ok; ++j) {
-        if constexpr (NS == 2) {
-          if (j + 1 < nt) load_k(j + 1);
-          if (ok) load_v(j);
-        } else {
-          load_v(j);
-          if (ok && j + 1 < nt) load_k(j + 1);
-        }
+        if (j + 1 < nt) load_k(j + 1);
+        if (ok) load_v(j);
       }
       if (!ok) {   // wait for the copies in flight
         for (int i = max(0, pos - SL); i < pos; ++i)
@@ -336,7 +332,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       int pos = 0;
       bool ok = tc5::wait(qfull, 0, flags);
       auto product_s = [&](int j) {
-        const uint32_t d = tmem + D + (j % NS) * NB;
+        const uint32_t d = tmem + D + (j & 1) * NB;
         for (int i = 0; i < L::nk; ++i, ++pos) {
           ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);
           if (!ok) return;
@@ -349,13 +345,13 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
           }
           tc5::commit(empty + pos % SL);
         }
-        tc5::commit(sfull + j % NS);
+        tc5::commit(sfull + (j & 1));
       };
       auto product_o = [&](int j) {
-        ok = ok && tc5::wait(pready + j % NS, (j / NS) & 1, flags);
+        ok = ok && tc5::wait(pready + (j & 1), (j >> 1) & 1, flags);
         if (!ok) return;
         tc5::fence_after();
-        const uint32_t pb = tmem + D + (j % NS) * NB;
+        const uint32_t pb = tmem + D + (j & 1) * NB;
         for (int i = 0; i < L::nv; ++i, ++pos) {
           ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);
           if (!ok) return;
@@ -370,15 +366,10 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       };
       if (ok) product_s(0);
       for (int j = 0; j < nt && ok; ++j) {
-        if constexpr (NS == 2) {
-          // the next scores go over the weights of tile j - 1, whose product was issued before:
-          // products of one CTA run in the order of their issue
-          if (j + 1 < nt) product_s(j + 1);
-          if (ok) product_o(j);
-        } else {
-          product_o(j);
-          if (ok && j + 1 < nt) product_s(j + 1);
-        }
+        // the next scores go over the weights of tile j - 1, whose product was issued before:
+        // products of one CTA run in the order of their issue
+        if (j + 1 < nt) product_s(j + 1);
+        if (ok) product_o(j);
       }
       if (!ok) {   // what was issued must end before the memory is given back
         flags[0] = 1;
@@ -396,10 +387,10 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     float m = kNegInf, l = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; ++j) {
-      ok = warp_wait(sfull + j % NS, (j / NS) & 1, flags);
+      ok = warp_wait(sfull + (j & 1), (j >> 1) & 1, flags);
       if (!ok) break;
       tc5::fence_after();
-      const uint32_t sb = lanes + D + (j % NS) * NB;
+      const uint32_t sb = lanes + D + (j & 1) * NB;
       const int t0 = (j0 + j) * NB;
       const bool edge = t0 + NB > lim_min;
       const int left = limit - t0;   // columns that the row sees
@@ -450,7 +441,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         // a slot's phase is told by its parity: the load before the one waited for must be known
         // to be over, and it is once the product of the tile before is
         if (j > 0) ok = warp_wait(odone + ((j - 1) & 1), (j - 1) >> 1 & 1, flags);
-        const int at = (NS == 2 ? min(j + 2, nt) : j + 1) * L::nk + j * L::nv;
+        const int at = min(j + 2, nt) * L::nk + j * L::nv;   // loaded before it
         for (int i = 0; i < L::nv; ++i) {
           const int pos = at + i;
           ok = ok && warp_wait(full + pos % SL, (pos / SL) & 1, flags);
@@ -463,7 +454,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       }
       tc5::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(pready + j % NS);   // one per warp: arrivals of lanes queue up
+      if (lane == 0) mbar_arrive(pready + (j & 1));   // one per warp: arrivals of lanes queue up
     }
     if (ok && nt > 0) ok = warp_wait(odone + ((nt - 1) & 1), (nt - 1) >> 1 & 1, flags);
     if (!ok) flags[0] = 1;
@@ -520,8 +511,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     if (live) {
       if (whole) {
         if (a.lse)
-          a.lse[row] = m == kNegInf ? kNegInf
-                                    : (m - tc5::kOff + log2f(l)) * 0.6931471805599453f;
+          a.lse[row] = l == 0.f ? kNegInf : (m - tc5::kOff + log2f(l)) * 0.6931471805599453f;
       } else {
         part[D] = m;
         part[D + 1] = l;
@@ -612,7 +602,7 @@ prompt_join_kernel(const __grid_constant__ PromptArgs a) {
       *reinterpret_cast<uint2*>(a.out + row * D + t * 4) =
           make_uint2(tc5::pack2<BF>(O.x * inv, O.y * inv), tc5::pack2<BF>(O.z * inv, O.w * inv));
       if (a.lse && t == 0)
-        a.lse[row] = M == kNegInf ? kNegInf : (M - tc5::kOff + log2f(l)) * 0.6931471805599453f;
+        a.lse[row] = l == 0.f ? kNegInf : (M - tc5::kOff + log2f(l)) * 0.6931471805599453f;
     }
   }
 }
@@ -631,7 +621,7 @@ Plan plan_for(int nseq, int total_q, int num_q_heads, int num_kv_heads, int D, i
   const int64_t per = (static_cast<int64_t>(max_q) + p.tpt - 1) / p.tpt;
   const int64_t a = static_cast<int64_t>(nseq) * per, b = total_q / p.tpt + static_cast<int64_t>(nseq);
   p.units = (a < b ? a : b) * num_kv_heads;
-  const int tiles = (max_k + nb - 1) / nb;
+  const int64_t tiles = (static_cast<int64_t>(max_k) + nb - 1) / nb;
   const int64_t slots = static_cast<int64_t>(sm_count() > 0 ? sm_count() : 152) * ctas;
   // Split only while the units leave SMs idle, and not below four tiles per split: a split costs
   // its start (about the time of two tiles) and its partial rows.
@@ -641,7 +631,7 @@ Plan plan_for(int nseq, int total_q, int num_q_heads, int num_kv_heads, int D, i
   if (want < 1) want = 1;
   p.tps = static_cast<int>((tiles + want - 1) / want);
   if (p.tps < 1) p.tps = 1;
-  p.n_splits = tiles > 0 ? (tiles + p.tps - 1) / p.tps : 1;
+  p.n_splits = tiles > 0 ? static_cast<int>((tiles + p.tps - 1) / p.tps) : 1;
   return p;
 }
 
@@ -759,8 +749,11 @@ extern "C" kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_
                 fn);
   if (nseq < 0 || total_q < 0 || total_k < 0 || max_q < 0 || max_k < 0)
     return fail(KVQ_ERR_RANGE, "%s: a count is negative", fn);
-  if (!std::isfinite(softmax_scale) || softmax_scale <= 0)
-    return fail(KVQ_ERR_RANGE, "%s: softmax_scale is not a finite value > 0", fn);
+  if (total_k > INT32_MAX - kRows)
+    return fail(KVQ_ERR_RANGE, "%s: total_k %d > 2^31 - 129", fn, total_k);
+  const float c = softmax_scale * 1.4426950408889634f;   // of scores in powers of 2
+  if (!std::isfinite(c) || softmax_scale <= 0)
+    return fail(KVQ_ERR_RANGE, "%s: softmax_scale is not a finite value > 0 (2.3e38 at most)", fn);
   if (nseq == 0 || total_q == 0 || max_q == 0) return ok();
   if (!q || !cu_q || !cu_k || !out || !workspace || (total_k > 0 && (!k || !v)))
     return fail(KVQ_ERR_NULL, "%s: NULL pointer", fn);
@@ -780,7 +773,7 @@ extern "C" kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_
   a.ws = static_cast<float*>(workspace); a.err = dev_err; a.nseq = nseq; a.total_q = total_q;
   a.total_k = total_k; a.max_q = max_q; a.max_k = max_k; a.Hq = num_q_heads; a.H = num_kv_heads;
   a.G = num_q_heads / num_kv_heads; a.tpt = p.tpt; a.n_splits = p.n_splits; a.tps = p.tps;
-  a.c = softmax_scale * 1.4426950408889634f;
+  a.c = c;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   auto go = [&](auto bf, auto d) {
     return launch<decltype(bf)::value, decltype(d)::value>(fn, a, p, q, q_stride, k, k_stride, v,

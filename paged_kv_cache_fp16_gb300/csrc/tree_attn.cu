@@ -1009,8 +1009,11 @@ extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_p
     return fail(KVQ_ERR_RANGE, "%s: max_nodes %d not in [1, %d]", fn, max_nodes, KVQ_MAX_NODES);
   if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_pages) * k0.page_size)
     return fail(KVQ_ERR_RANGE, "%s: max_seq_len exceeds max_pages * page_size", fn);
-  if (!std::isfinite(softmax_scale) || softmax_scale <= 0)
-    return fail(KVQ_ERR_RANGE, "%s: softmax_scale is not a finite value > 0", fn);
+  if (max_seq_len > INT32_MAX - kTile)
+    return fail(KVQ_ERR_RANGE, "%s: max_seq_len %d > 2^31 - 65", fn, max_seq_len);
+  const float c = softmax_scale * 1.4426950408889634f;   // of scores in powers of 2
+  if (!std::isfinite(c) || softmax_scale <= 0)
+    return fail(KVQ_ERR_RANGE, "%s: softmax_scale is not a finite value > 0 (2.3e38 at most)", fn);
   if (nseq == 0 || total_nodes == 0) return ok();
   if (!q || !page_table || !seq_lens || !cu_nodes || !parents || !out || !workspace)
     return fail(KVQ_ERR_NULL, "%s: NULL pointer", fn);
@@ -1038,7 +1041,7 @@ extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_p
   a.G = num_q_heads / H; a.ps = k0.page_size; a.max_pages = max_pages; a.max_nodes = max_nodes;
   a.max_len = max_seq_len; a.tpt = p.tpt; a.grid = p.grid; a.whole = p.whole ? 1 : 0;
   a.cuts = reinterpret_cast<Cut*>(a.ws + static_cast<int64_t>(p.grid) * 2 * kRec);
-  a.c = softmax_scale * 1.4426950408889634f;
+  a.c = c;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = k0.bits == 8 ? launch<8>(a, p, cs)
                         : k0.bits == 6 ? launch<6>(a, p, cs) : launch<4>(a, p, cs);

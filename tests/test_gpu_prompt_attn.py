@@ -229,3 +229,28 @@ def test_a_chunk_joined_to_earlier_keys_by_lse_is_the_whole(kvq, cuda_dev):
     l = torch.logaddexp(la, lb)
     joined = a.float() * (la - l).exp()[..., None] + b.float() * (lb - l).exp()[..., None]
     assert torch.allclose(l, lw, atol=1e-5) and torch.allclose(joined, whole.float(), atol=1e-3)
+
+
+@pytest.mark.parametrize("D", [64, 256])
+def test_bounds_far_above_the_lengths(kvq, cuda_dev, D):
+    new, keys = [1, 40], [300, 900]
+    q, k, v = _inputs(cuda_dev, "f16", new, keys, 6, 1, D, 31)
+    exact, lse, _ = _call(kvq, q, k, v, new, keys, 0.1)
+    far, far_lse, err = _call(kvq, q, k, v, new, keys, 0.1, max_q=2 ** 31 - 1, max_k=2 ** 31 - 1)
+    assert err == 0
+    # one split instead of several: the same sums in another order, each result rounded once
+    f = [x.double().cpu().numpy() for x in (q, k, v)]
+    r = op.prompt_attention(*f, cu_of(new), cu_of(keys), 0.1)
+    for o, s in ((exact, lse), (far, far_lse)):
+        assert_rows_close(o.double().cpu().numpy(), r["out"], r["size"], r["span"], "f16")
+        assert_lse_close(s.cpu().numpy(), r["lse"], r["span"], D)
+
+
+@pytest.mark.parametrize("keys", [90, 5000])
+def test_lse_of_a_row_of_nan_scores_is_nan(kvq, cuda_dev, keys):
+    q, k, v = _inputs(cuda_dev, "f16", [90], [keys], 6, 1, 256, 33)
+    q[40, 2] = float("nan")
+    out, lse, err = _call(kvq, q, k, v, [90], [keys], 0.0625)
+    assert err == 0 and torch.isnan(out[40, 2]).all()
+    bad = torch.isnan(lse)
+    assert bad[40, 2] and int(bad.sum()) == 1 and torch.isfinite(lse[~bad]).all()

@@ -145,3 +145,31 @@ def test_host_tensors_are_refused_by_the_binding(kvq):
         kvq.kvq_tree_attn([pool], [pool], q, i[None], i[:1], i, i[:1], 1, 16, 1.0, q, i)
     with pytest.raises(TypeError):
         kvq.kvq_tree_commit([pool], i[None], i[:1], i, i)
+
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(scale=3e38), RANGE),                    # finite, but not once it is in powers of two
+    (dict(tk=BIG), RANGE), (dict(tk=BIG - 127), RANGE)])
+def test_prompt_refuses_the_ends_of_the_range(kvq, over, status):
+    assert _call(kvq, "kvq_prompt_attn", _prompt(kvq), **over) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(scale=3e38), RANGE), (dict(ml=BIG, mp=BIG), RANGE), (dict(ml=BIG - 63, mp=BIG), RANGE),
+    # 2^30 tiles: 2 sequences x 2 heads x 1 row tile x 2^31 / 64 tokens x 9 layers and more
+    (dict(ml=BIG - 64, mp=BIG, n=9, k=9, v=9, wsb=1 << 40), RANGE)])
+def test_tree_refuses_the_ends_of_the_range(kvq, over, status):
+    over = {k: _pools(kvq, x) if k in ("k", "v") else x for k, x in over.items()}
+    assert _call(kvq, "kvq_tree_attn", _tree(kvq), **over) == status
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_generous_bounds_plan_like_exact_ones(kvq, D):
+    # 128 keys below 2^31 are one tile fewer: the plans differ by no more than their rounding
+    a = kvq.kvq_prompt_attn_workspace(1, 1, 6, 1, D, 1, BIG)
+    b = kvq.kvq_prompt_attn_workspace(1, 1, 6, 1, D, 1, BIG - 1000)
+    assert a == b > kvq.kvq_prompt_attn_workspace(1, 1, 6, 1, D, 1, 100)
+    assert kvq.kvq_prompt_attn_workspace(2, 9, 6, 1, D, BIG, 100) > 0
