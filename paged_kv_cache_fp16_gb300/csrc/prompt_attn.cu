@@ -348,12 +348,13 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         tc5::commit(sfull + (j & 1));
       };
       auto product_o = [&](int j) {
+        ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);   // sooner than the weights
         ok = ok && tc5::wait(pready + (j & 1), (j >> 1) & 1, flags);
         if (!ok) return;
         tc5::fence_after();
         const uint32_t pb = tmem + D + (j & 1) * NB;
         for (int i = 0; i < L::nv; ++i, ++pos) {
-          ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);
+          if (i > 0) ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);
           if (!ok) return;
           const uint32_t vb = ring + (pos % SL) * L::kSlot;
 #pragma unroll
