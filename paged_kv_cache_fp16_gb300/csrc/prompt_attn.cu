@@ -84,6 +84,7 @@ struct PromptArgs {
   int n_splits;   // CTAs along the keys
   int tps;        // key tiles per split
   float c;        // softmax_scale * log2(e)
+  float inv;      // softmax_scale / c: from powers of 2 back, c's own rounding taken out
 };
 
 // One row tile of one KV head of one sequence.
@@ -196,6 +197,13 @@ template <bool BF> __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   if ((w & e) == e) w &= 0xffff0000u;
   if ((w & (e << 16)) == (e << 16)) w &= 0x0000ffffu;
   return w;
+}
+
+// ln sum exp of a row from its reference m (in powers of 2) and its sum of 2^(s c - m + kOff).
+__device__ __forceinline__ float row_lse(const PromptArgs& a, float m, float l) {
+  constexpr float unit = 1.f / 1024.f;   // 2^-kOff: the offset goes out without a rounding
+  static_assert(tc5::kOff == 10.f, "2^kOff");
+  return l == 0.f ? kNegInf : (m + log2f(l * unit)) * a.inv;
 }
 
 // A whole warp's bounded wait: every lane goes the same way on.
@@ -512,7 +520,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     if (live) {
       if (whole) {
         if (a.lse)
-          a.lse[row] = l == 0.f ? kNegInf : (m - tc5::kOff + log2f(l)) * 0.6931471805599453f;
+          a.lse[row] = row_lse(a, m, l);
       } else {
         part[D] = m;
         part[D + 1] = l;
@@ -603,7 +611,7 @@ prompt_join_kernel(const __grid_constant__ PromptArgs a) {
       *reinterpret_cast<uint2*>(a.out + row * D + t * 4) =
           make_uint2(tc5::pack2<BF>(O.x * inv, O.y * inv), tc5::pack2<BF>(O.z * inv, O.w * inv));
       if (a.lse && t == 0)
-        a.lse[row] = l == 0.f ? kNegInf : (M - tc5::kOff + log2f(l)) * 0.6931471805599453f;
+        a.lse[row] = row_lse(a, M, l);
     }
   }
 }
@@ -775,6 +783,7 @@ extern "C" kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_
   a.total_k = total_k; a.max_q = max_q; a.max_k = max_k; a.Hq = num_q_heads; a.H = num_kv_heads;
   a.G = num_q_heads / num_kv_heads; a.tpt = p.tpt; a.n_splits = p.n_splits; a.tps = p.tps;
   a.c = c;
+  a.inv = static_cast<float>(static_cast<double>(softmax_scale) / c);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   auto go = [&](auto bf, auto d) {
     return launch<decltype(bf)::value, decltype(d)::value>(fn, a, p, q, q_stride, k, k_stride, v,

@@ -1,8 +1,9 @@
 // Attention of a tree of drafted tokens over the packed pages, on the fifth-generation tensor
 // cores.
 //
-// The rows of a tile are (draft, grouped query head) pairs of one KV head, 128 at most; per tile
-// of 64 tokens the packed codes are brought in once and become fp16 in shared memory, exactly as
+// A sequence's (draft, grouped query head) pairs of one KV head, draft by draft, are cut into row
+// tiles of 128 (a draft's heads may lie in two: 64 drafts of 6 heads fill 3 tiles); per tile of 64
+// tokens the packed codes are brought in once and become fp16 in shared memory, exactly as
 // the dequantizer rounds them (k_hat = fp16(c * scale)):
 //   S = Q K_hat^T       tcgen05.mma, Q (fp16) in TMEM, K_hat in shared memory
 //   p = 2^(S c - m)     two threads per row, running maximum and sum; drafts outside the row's
@@ -63,7 +64,8 @@ struct TreePools {
 // What a CTA leaves of the unit that its share cuts at the tail (the unit's first record): the
 // join needs no search.  n = 0: none.
 struct Cut {
-  int n, row0, stride, tokens;   // records from this CTA on; first row of out, rows per draft, drafts
+  int n, row0, first, rows;   // records from this CTA on; out's row of the unit's sequence and KV
+                              // head; the row tile's first row and its rows
 };
 
 struct TreeArgs {
@@ -77,7 +79,6 @@ struct TreeArgs {
   const int32_t* parents;
   int32_t* err;
   int n_layers, nseq, total, H, Hq, G, ps, max_pages, max_nodes, max_len;
-  int tpt;      // drafts per row tile
   int grid;     // CTAs of the attention kernel
   int whole;    // deal whole units (short caches)
   Cut* cuts;    // [grid]
@@ -121,7 +122,7 @@ __device__ __forceinline__ Seq seq_of(const TreeArgs& a, int s, bool check) {
     q.len = len;
     if (q.n > 0) {
       q.tiles = (len + q.n + kTile - 1) / kTile;
-      q.rt = (q.n + a.tpt - 1) / a.tpt;
+      q.rt = (q.n * a.G + kRows - 1) / kRows;
     }
   } else if (check) {
     report(a.err, KVQ_DEVERR_INDEX);
@@ -373,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       if (u.start >= w.at && u.start + u.q.tiles > w.end)
         cut = Cut{static_cast<int>((u.start + u.q.tiles - 1) / share_of(a, w.layer_tiles)) -
                       static_cast<int>(blockIdx.x) + 1,
-                  (u.l * a.total + u.q.n0 + u.r * a.tpt) * a.Hq + u.h * a.G, a.Hq,
-                  min(a.tpt, u.q.n - u.r * a.tpt)};
+                  (u.l * a.total + u.q.n0) * a.Hq + u.h * a.G, u.r * kRows,
+                  min(kRows, u.q.n * a.G - u.r * kRows)};
     }
     if (lane == 0) a.cuts[blockIdx.x] = cut;
   }
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     }
   } else {
     // ------------------------------------- softmax: two threads per row, half the columns each
-    const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane, ri = r / a.G;
+    const int quad = warp & 3, half = warp >> 2, r = quad * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad) << 21);
     // the other half's value, through shared memory: the row's two warps meet after the write and
     // after the read
@@ -659,11 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
     };
     while (ok && next_segment(a, w, g)) {
       const Seq& q = g.u.q;
-      const int node = g.u.r * a.tpt + ri;
-      const bool live = ri < a.tpt && node < q.n;
+      const int node = (g.u.r * kRows + r) / a.G;
+      const bool live = node < q.n;
       const bool idle = !__any_sync(kFullMask, live);
       const int64_t row = (static_cast<int64_t>(g.u.l) * a.total + q.n0 + node) * a.Hq +
-                          g.u.h * a.G + (r - ri * a.G);
+                          g.u.h * a.G + (g.u.r * kRows + r - node * a.G);
       // Q of this row into TMEM, channels in the stored order
 #pragma unroll 1
       for (int b = half * 2; b < half * 2 + 2; ++b) {
@@ -866,8 +867,8 @@ tree_join_kernel(const __grid_constant__ TreeArgs a) {
   const Cut cut = a.cuts[mine];
   const int c0 = mine, c1 = c0 + cut.n - 1;
   const int r = threadIdx.x % kRows, slice = threadIdx.x / kRows, col = blockIdx.y * kJoinCols;
-  const int ri = r / a.G;
-  const bool live = ri < cut.tokens;
+  const int node = (cut.first + r) / a.G;
+  const bool live = r < cut.rows;
   float M = kNegInf, l = 0.f, O[kJoinCols];
 #pragma unroll
   for (int e = 0; e < kJoinCols; ++e) O[e] = 0.f;
@@ -910,7 +911,7 @@ tree_join_kernel(const __grid_constant__ TreeArgs a) {
     for (int e = 0; e < kJoinCols; ++e) O[e] = fmaf(part_sm[i][e][r], f, O[e]);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t row = static_cast<int64_t>(cut.row0) + ri * cut.stride + (r - ri * a.G);
+  const int64_t row = static_cast<int64_t>(cut.row0) + node * a.Hq + (cut.first + r - node * a.G);
   uint32_t y[kJoinCols / 2];
 #pragma unroll
   for (int e = 0; e < kJoinCols; e += 2) y[e / 2] = pack_h2(O[e] * inv, O[e + 1] * inv);
@@ -922,16 +923,17 @@ tree_join_kernel(const __grid_constant__ TreeArgs a) {
 
 // How a call is cut; the units are an upper bound (the lengths are on the device).
 struct Plan {
-  int tpt, grid;
+  int grid;
   bool whole;
   int64_t units;
 };
 
 Plan plan_for(int n_layers, int nseq, int total_nodes, int H, int Hq, int max_nodes, int max_len) {
   Plan p;
-  p.tpt = kRows / (Hq / H);
-  const int64_t per = (max_nodes + p.tpt - 1) / p.tpt;
-  const int64_t a = static_cast<int64_t>(nseq) * per, b = total_nodes / p.tpt + static_cast<int64_t>(nseq);
+  const int G = Hq / H;
+  const int64_t per = (max_nodes * G + kRows - 1) / kRows;
+  const int64_t a = static_cast<int64_t>(nseq) * per;
+  const int64_t b = static_cast<int64_t>(total_nodes) * G / kRows + nseq;
   p.units = (a < b ? a : b) * H * n_layers;
   const int64_t tiles = (static_cast<int64_t>(max_len) + kTile - 1) / kTile;
   p.whole = tiles <= kShortTiles;
@@ -1039,7 +1041,7 @@ extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_p
   a.lens = seq_lens; a.cu = cu_nodes; a.parents = parents; a.err = dev_err;
   a.n_layers = n_layers; a.nseq = nseq; a.total = total_nodes; a.H = H; a.Hq = num_q_heads;
   a.G = num_q_heads / H; a.ps = k0.page_size; a.max_pages = max_pages; a.max_nodes = max_nodes;
-  a.max_len = max_seq_len; a.tpt = p.tpt; a.grid = p.grid; a.whole = p.whole ? 1 : 0;
+  a.max_len = max_seq_len; a.grid = p.grid; a.whole = p.whole ? 1 : 0;
   a.cuts = reinterpret_cast<Cut*>(a.ws + static_cast<int64_t>(p.grid) * 2 * kRec);
   a.c = c;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

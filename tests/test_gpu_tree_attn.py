@@ -352,3 +352,11 @@ def test_a_speculative_step_end_to_end(kvq, cuda_dev):
     want = torch.empty_like(got)
     kvq.kvq_decode_attn([kq], [vq], q1, pt, after, 60, 1 / 16, want, ws)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("bits", [8, 6, 4])
+@pytest.mark.parametrize("G", [3, 5, 6, 7, 16])
+def test_row_tiles_that_cut_a_drafts_heads(kvq, cuda_dev, bits, G):
+    nodes = [64, 43, 22, 21, 1]
+    _check(kvq, cuda_dev, bits, 2, G, [70, 300, 5, 0, 129], nodes, seed=50 + G)     # whole units
+    _check(kvq, cuda_dev, bits, 2, G, [2600, 300, 1500, 0, 129], nodes, ps=32, seed=60 + G, tail=1)
