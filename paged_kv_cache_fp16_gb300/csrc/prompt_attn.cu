@@ -14,9 +14,14 @@
 // pieces along the channels, a V tile as pieces along its keys, each of which is handed back when
 // its products are done.
 //
-// Per head dimension (measured on one GB300, figures beside the launch table below): at 256, O and
-// two score buffers fill TMEM, one CTA per SM, and the softmax of one tile runs under the products
-// of the next; at 128 and 64 two CTAs share an SM and cover each other's softmax.
+// Per head dimension: at 256, O and two score buffers of 128 keys fill TMEM, one CTA per SM, and
+// the softmax of one tile runs under the products of the next; at 128 and 64 two CTAs share an SM
+// and cover each other's softmax.  What bounds it (one GB300, whole prompts of 16,384 tokens): at
+// 256 the tensor cores (1,690 to 1,815 TFLOP/s in fp16, 1,740 to 1,900 in bf16, by the chip's
+// power); at 128 the tensor cores fed from shared memory (a product of 128 x 64 x 16 with both
+// operands there takes 48 cycles, not 32; 1,300 to 1,450 TFLOP/s); at 64 the softmax's chain of
+// waits, exponentials and stores, 1,340 cycles per tile and CTA (850 to 990 TFLOP/s, tensor and
+// exponential units 35-40 % busy).  One token over 131,000 keys at 256 channels: 86 us, 6.26 TB/s.
 //
 // Keys that a row does not see: scores are set to -inf whatever they hold; in the tiles where some
 // row's view ends, V rows that no row sees are zeroed and non-finite V values that only some rows
@@ -49,7 +54,10 @@ constexpr int kThreads = 192;
 constexpr int kScores = 2;   // score buffers
 
 // NB: keys per tile.  KD: channels of a K slot (NB rows).  VR: keys of a V slot (D channels).
-// kSlots: ring slots.  kCtas: resident CTAs per SM.
+// kSlots: ring slots.  kCtas: resident CTAs per SM.  Two score buffers each.
+// Measured against each other (16,384 tokens, TFLOP/s): at 128 channels one buffer of 128 keys
+// 1,049, two of 64 1,354; at 64 channels two of 64 in 2 CTAs 972, one of 128 in 2 CTAs 790, two of
+// 128 in 1 CTA 749, one of 64 in 4 CTAs 848; three buffers of 64 as fast as two.
 template <int D> struct Cfg;
 template <> struct Cfg<256> { static constexpr int NB = 128, KD = 128, VR = 64, kSlots = 5, kCtas = 1; };
 template <> struct Cfg<128> { static constexpr int NB = 64, KD = 128, VR = 64, kSlots = 5, kCtas = 2; };

@@ -16,6 +16,16 @@
 // bring codes and scales of K and of V (16-token groups of a page) into rings deep enough to cover
 // the memory latency, 8 unpack.
 //
+// What bounds it: per tile of 64 tokens shared memory moves 178 KB at q6 (codes in and out, K_hat
+// and V_hat in and out: 1,390 cycles), the unpacking and the softmax issue 5,300 warp instructions
+// (1,340 cycles of the four schedulers), the products take 1,024 and the codes' arrival 1,060; they
+// overlap to 2,450 cycles, the unpacking warps being busy for 2,000 of them (reads, arithmetic and
+// the waits for the double buffers, which fill shared memory).  262,000 tokens and 16 drafts of 6
+// heads: q6 138 us (2.95 TB/s, 746 TFLOP/s), q4 129 us; 8 x 20,000 tokens q8, 10 drafts 98 us
+// (3.4 TB/s), 64 drafts (3 row tiles) 268 us.  Measured against this: 16 unpacking warps (fewer
+// registers each) and 4 softmax warps slower; two copying warps for each of K and V leave 80
+// registers, 158 us.
+//
 // Work: the tiles of all (layer, sequence, KV head, row tile) units in one line are dealt to the
 // CTAs in equal contiguous shares, whatever the sequences' lengths (which only the device knows).
 // A unit that lies inside one share is finished there; the at most two cut units of a share leave
