@@ -68,6 +68,11 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
                : "memory");
 }
 
+// Brings a tensor map to where the copies look for it.
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ void fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
