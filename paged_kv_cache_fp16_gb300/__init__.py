@@ -756,14 +756,21 @@ def _device(t, name: str) -> int:
     return dev
 
 
-def _here(t, name: str, dev: int, dtype=None, dims: int | None = None) -> int:
-    """The address of a contiguous tensor of device `dev`."""
+def _refuse(t, name: str, dev: int, dtype) -> None:
+    """Raises what is wrong with a tensor's kind, type or device, if it is one of these."""
     if not isinstance(t, torch.Tensor) or t.get_device() < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
+
+
+def _here(t, name: str, dev: int, dtype=None, dims: int | None = None) -> int:
+    """The address of a contiguous tensor of device `dev`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or (
+            dtype is not None and t.dtype is not dtype):
+        _refuse(t, name, dev, dtype)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dims is not None and t.dim() != dims:
@@ -775,22 +782,18 @@ def _opt(t, name: str, dev: int, dtype, dims: int | None = None) -> int | None:
     return None if t is None else _here(t, name, dev, dtype, dims)
 
 
-def _head_rows(t, name: str, dev: int, dtype) -> tuple[int, int]:
+def _head_rows(t, name: str, dev: int, dtype) -> tuple[int, int, int, int, int]:
     """Checks [tokens, heads, D] rows of `dtype`, a token's heads contiguous, and returns their
-    address and the elements between tokens."""
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    address, the elements between tokens, and the three sizes."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype:
+        _refuse(t, name, dev, dtype)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     n, h, d = t.shape
     sn, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.data_ptr(), (sn if n > 1 else -(-h * d // 8) * 8)
+    return t.data_ptr(), (sn if n > 1 else -(-h * d // 8) * 8), n, h, d
 
 
 def _raw_stream(stream, dev: int) -> int:
@@ -831,27 +834,25 @@ def kvq_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_out: torch.Tensor, k_ou
     dev, dt = _device(q, "q"), q.dtype
     if dt not in _DTYPES:
         raise TypeError(f"q must be float16 or bfloat16, got {dt}")
-    qp, qs = _head_rows(q, "q", dev, dt)
-    kp, ks = _head_rows(k, "k", dev, dt)
-    qop, qos = (qp, qs) if q_out is q else _head_rows(q_out, "q_out", dev, dt)
-    kop, kos = (kp, ks) if k_out is k else _head_rows(k_out, "k_out", dev, dt)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
+    qp, qs, n, hq, d = rows_q = _head_rows(q, "q", dev, dt)
+    kp, ks, nk, h, dk = rows_k = _head_rows(k, "k", dev, dt)
+    qop, qos, *q_shape = rows_q if q_out is q else _head_rows(q_out, "q_out", dev, dt)
+    kop, kos, *k_shape = rows_k if k_out is k else _head_rows(k_out, "k_out", dev, dt)
+    if q_shape != [n, hq, d] or k_shape != [nk, h, dk]:
         raise ValueError("q_out / k_out must have q's / k's shape")
-    n, hq, d = q.shape
-    if k.shape[0] != n or k.shape[2] != d:
+    if nk != n or dk != d:
         raise ValueError("q and k must have the same tokens and head_dim")
-    if positions.shape != (n,):
+    pos = _here(positions, "positions", dev, torch.int32)
+    if positions.dim() != 1 or positions.size(0) != n:
         raise ValueError("one position per token")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.shape != (d,):
-            raise ValueError(f"{name} must have head_dim entries")
-    _check(_lib.kvq_qk_norm_rope(_DTYPES[dt], qp, qs, kp, ks, qop, qos, kop, kos, n, hq, k.shape[1],
-                                 d, 0 if phases is None else 2 * phases.numel(),
-                                 1 if interleaved else 0,
-                                 _here(positions, "positions", dev, torch.int32),
-                                 _opt(phases, "phases", dev, torch.int64, 1),
-                                 _opt(q_weight, "q_weight", dev, torch.float32),
-                                 _opt(k_weight, "k_weight", dev, torch.float32), eps,
+    qw = _opt(q_weight, "q_weight", dev, torch.float32)
+    kw = _opt(k_weight, "k_weight", dev, torch.float32)
+    if (qw is not None and q_weight.shape != (d,)) or (kw is not None and k_weight.shape != (d,)):
+        raise ValueError("a weight must have head_dim entries")
+    _check(_lib.kvq_qk_norm_rope(_DTYPES[dt], qp, qs, kp, ks, qop, qos, kop, kos, n, hq, h, d,
+                                 0 if phases is None else 2 * phases.numel(),
+                                 1 if interleaved else 0, pos,
+                                 _opt(phases, "phases", dev, torch.int64, 1), qw, kw, eps,
                                  _raw_stream(stream, dev)))
 
 
@@ -878,17 +879,15 @@ def kvq_prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: tor
     dev, dt = _device(q, "q"), q.dtype
     if dt not in _DTYPES:
         raise TypeError(f"q must be float16 or bfloat16, got {dt}")
-    qp, qs = _head_rows(q, "q", dev, dt)
-    kp, ks = _head_rows(k, "k", dev, dt)
-    vp, vs = _head_rows(v, "v", dev, dt)
-    n, hq, d = q.shape
-    total_k, h, dk = k.shape
-    if k.shape != v.shape or dk != d:
+    qp, qs, n, hq, d = _head_rows(q, "q", dev, dt)
+    kp, ks, total_k, h, dk = _head_rows(k, "k", dev, dt)
+    vp, vs, nv, hv, dv = _head_rows(v, "v", dev, dt)
+    if nv != total_k or hv != h or dv != dk or dk != d:
         raise ValueError("k and v must have one shape, and q's head_dim")
-    if out.shape != q.shape:
+    if out.shape != (n, hq, d):
         raise ValueError("out must have q's shape")
-    nseq = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
-    if nseq < 0 or cu_k.shape != cu_q.shape:
+    nseq = cu_q.size(0) - 1 if cu_q.dim() == 1 else -1
+    if nseq < 0 or cu_k.shape != (nseq + 1,):
         raise ValueError("cu_q and cu_k must have nseq + 1 entries each")
     if lse is not None and lse.shape != (n, hq):
         raise ValueError("lse must be [total_q, Hq]")
@@ -922,10 +921,10 @@ def tree_workspace(k_pools: Sequence[Pool], nseq: int, total_nodes: int, num_q_h
 
 def _tree_table(page_table, seq_lens, cu) -> int:
     """Checks the shapes of what describes a tree call's sequences; returns their count."""
-    if seq_lens.dim() != 1 or page_table.dim() != 2 or page_table.shape[0] < seq_lens.shape[0] \
-            or cu.shape != (seq_lens.shape[0] + 1,):
+    nseq = seq_lens.size(0) if seq_lens.dim() == 1 else -1
+    if nseq < 0 or page_table.dim() != 2 or page_table.size(0) < nseq or cu.shape != (nseq + 1,):
         raise ValueError("page_table needs a row per sequence and the offsets nseq + 1 entries")
-    return seq_lens.shape[0]
+    return nseq
 
 
 def kvq_tree_attn(k_pools: Sequence[Pool], v_pools: Sequence[Pool], q: torch.Tensor,
