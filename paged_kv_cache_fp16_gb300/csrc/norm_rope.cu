@@ -11,7 +11,8 @@
 // it, so a warp holds 1, 2 or 4 rows of 256, 128 or 64 channels).  A lane's channels are two runs
 // of 4 so chosen that both channels of a pair are its own: for pairs half a rotated part apart,
 // one run from each half; a row then costs two 8-byte loads and stores and no exchange but the
-// mean's shuffle tree.
+// mean's shuffle tree.  For neighbouring pairs the runs are neighbours too and move as 16 bytes
+// (5,003 tokens of 40 rows of 64 channels: 17.1 us as two loads, 16.3 so).
 //
 // What bounds it is the arithmetic as much as the memory: 32,768 tokens of 28 rows of 256 channels
 // (940 MB) would take 139 us at the copy rate.  Measured there: with the partner's channels
@@ -100,6 +101,7 @@ constexpr int kThreads = 128;
 constexpr int kU = 4;   // rows in flight per group of lanes
 
 // Rows r0 .. r0 + kU - 1 of the n at x (D apart).
+template <bool INTER>
 __device__ __forceinline__ void load_rows(const Lane& L, const NormRopeArgs& a, const uint16_t* x,
                                           int r0, int n, uint2 v[kU][2]) {
 #pragma unroll
@@ -107,8 +109,14 @@ __device__ __forceinline__ void load_rows(const Lane& L, const NormRopeArgs& a, 
     v[u][0] = v[u][1] = make_uint2(0, 0);
     if (L.live && r0 + u < n) {
       const uint16_t* p = x + static_cast<int64_t>(r0 + u) * a.D;
-      v[u][0] = *reinterpret_cast<const uint2*>(p + L.a);
-      v[u][1] = *reinterpret_cast<const uint2*>(p + L.b);
+      if constexpr (INTER) {   // the runs are neighbours
+        const uint4 w = *reinterpret_cast<const uint4*>(p + L.a);
+        v[u][0] = make_uint2(w.x, w.y);
+        v[u][1] = make_uint2(w.z, w.w);
+      } else {
+        v[u][0] = *reinterpret_cast<const uint2*>(p + L.a);
+        v[u][1] = *reinterpret_cast<const uint2*>(p + L.b);
+      }
     }
   }
 }
@@ -122,7 +130,7 @@ __device__ __forceinline__ void rows(const Lane& L, const NormRopeArgs& a, const
   const float inv_d = 1.f / static_cast<float>(a.D);
 #pragma unroll 1
   for (int r0 = 0; r0 < n_max; r0 += kU) {
-    if (r0 > 0) load_rows(L, a, x, r0, n, v);
+    if (r0 > 0) load_rows<INTER>(L, a, x, r0, n, v);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       float f[8];
@@ -172,8 +180,12 @@ __device__ __forceinline__ void rows(const Lane& L, const NormRopeArgs& a, const
         for (int i = 0; i < 4; ++i)
           w[i] = INTER ? tc5::pack2<BF>(g[i], g[i + 4]) : tc5::pack2<BF>(g[2 * i], g[2 * i + 1]);
         uint16_t* p = y + static_cast<int64_t>(r0 + u) * a.D;
-        *reinterpret_cast<uint2*>(p + L.a) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2*>(p + L.b) = make_uint2(w[2], w[3]);
+        if constexpr (INTER) {
+          *reinterpret_cast<uint4*>(p + L.a) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          *reinterpret_cast<uint2*>(p + L.a) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(p + L.b) = make_uint2(w[2], w[3]);
+        }
       }
     }
   }
@@ -224,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) norm_rope_kernel(co
     const uint16_t* xq = a.q + t * a.qs + static_cast<int64_t>(q0) * a.D;
     const uint16_t* xk = a.k + t * a.ks + static_cast<int64_t>(k0) * a.D;
     uint2 v[kU][2];   // the first rows are on their way while the factors are formed
-    if (mq > 0) load_rows(L, a, xq, 0, nq, v);
-    else load_rows(L, a, xk, 0, nk, v);
+    if (mq > 0) load_rows<INTER>(L, a, xq, 0, nq, v);
+    else load_rows<INTER>(L, a, xk, 0, nk, v);
     float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
     if (L.rot) {
       const int64_t p = __ldg(a.pos + t);
@@ -241,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) norm_rope_kernel(co
     if (mq > 0) {
       rows_of<BF, LPR, INTER>(L, a, c, s, xq, a.qo + t * a.qos + static_cast<int64_t>(q0) * a.D,
                               a.qw, nq, mq, v);
-      if (mk > 0) load_rows(L, a, xk, 0, nk, v);
+      if (mk > 0) load_rows<INTER>(L, a, xk, 0, nk, v);
     }
     if (mk > 0)
       rows_of<BF, LPR, INTER>(L, a, c, s, xk, a.ko + t * a.kos + static_cast<int64_t>(k0) * a.D,
