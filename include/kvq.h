@@ -560,8 +560,8 @@ KVQ_API kvq_status kvq_rope_phases(const double* inv_freq, int n, uint64_t* phas
  * and then its first rotary_dim values are rotated in pairs (a, b), pair i by the angle
  * positions[t] * inv_freq[i]:  a' = a cos - b sin,  b' = b cos + a sin, with (a, b) =
  * (y_i, y_{i + rotary_dim / 2}), or (y_{2i}, y_{2i+1}) if interleaved.  Computed in float32 from
- * the inputs, rounded once to the output type.  A row whose sum of squares exceeds float32 (bf16
- * values of 1e19 and more) becomes 0, a row of zeros with eps 0 NaN.
+ * the inputs, rounded once to the output type.  A row whose sum of squares leaves float32's
+ * range (bf16 values of 1e19 and more) gives 0 or NaN, a row of zeros with eps 0 NaN.
  * q, k           device, `dtype`, [num_tokens][heads][D], a token's heads contiguous, tokens
  *                q_stride / k_stride elements apart (a multiple of 8, >= heads * D): views into a
  *                fused projection's output are fine.  num_tokens may be 0.
