@@ -117,6 +117,13 @@ template <int BITS> __host__ __device__ constexpr int place(int e) {
          : BITS == 4 ? ((e & 3) << 1) | (e >> 2) : e;
 }
 
+// The channel at place p of an aligned group of 32: the inverse.
+template <int BITS> __host__ __device__ constexpr int channel(int p) {
+  for (int e = 0; e < 8; ++e)
+    if (place<BITS>(e) == (p & 7)) return (p & ~7) | e;
+  return p;
+}
+
 struct Seq {
   int n0, n, len, tiles, rt;   // first draft, drafts, cached tokens, token tiles, row tiles
 };
@@ -789,6 +796,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       l += other(l);
       const bool whole = g.count == q.tiles;
       const bool fix = drafts && flags[1] != 0;
+      if (fix) {   // apart from the rows' way out, which short calls run once, from cold
+#pragma unroll 1
+        for (int b = half * 4; b < half * 4 + 4; ++b) {
+          uint32_t o[32];
+          tc5::ld32(lanes + b * 32, o);
+          tc5::wait_ld32(o);
+          const TreePools& P = a.L[g.u.l];
+          const int lo = max(0, g.u.tile * kTile - q.len);
+          const int hi = min(q.n, (g.u.tile + g.count) * kTile - q.len);
+          for (int d = lo; d < hi; ++d) {
+            if (!(seen >> d & 1)) continue;
+            const int64_t at = locate_row(a.pt, a.max_pages, a.ps, a.H, P.v_pages, g.u.s,
+                                          static_cast<int64_t>(q.len) + d, g.u.h, nullptr);
+            if (at < 0) continue;
+            const float vs = h2f(P.vs[at]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {   // o[i]: the channel stored at place i
+              const float v = value_at<BITS>(P.vc + at * L::kPd, vs, b * 32 + channel<BITS>(i));
+              if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+            }
+          }
+          __syncwarp();
+          tc5::st32(lanes + b * 32, o);
+        }
+        tc5::wait_st();
+      }
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
       // a cut unit at the head of the share is its first record, one at the tail its second
       float* part = a.ws + (static_cast<int64_t>(blockIdx.x) * 2 + (g.u.tile > 0 ? 0 : 1)) * kRec;
@@ -803,23 +836,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           x[i] = __float_as_uint(__uint_as_float(o[(i & ~7) | place<BITS>(i & 7)]) * inv);
-        if (fix) {
-          const TreePools& P = a.L[g.u.l];
-          const int lo = max(0, g.u.tile * kTile - q.len);
-          const int hi = min(q.n, (g.u.tile + g.count) * kTile - q.len);
-          for (int d = lo; d < hi; ++d) {
-            if (!(seen >> d & 1)) continue;
-            const int64_t at = locate_row(a.pt, a.max_pages, a.ps, a.H, P.v_pages, g.u.s,
-                                          static_cast<int64_t>(q.len) + d, g.u.h, nullptr);
-            if (at < 0) continue;
-            const float vs = h2f(P.vs[at]);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float v = value_at<BITS>(P.vc + at * L::kPd, vs, b * 32 + i);
-              if (!isfinite(v)) x[i] = __float_as_uint(__uint_as_float(x[i]) + v);
-            }
-          }
-        }
         if (whole) {
           uint4* dst = reinterpret_cast<uint4*>(a.out + row * kD + b * 32);
 #pragma unroll

@@ -360,3 +360,26 @@ def test_row_tiles_that_cut_a_drafts_heads(kvq, cuda_dev, bits, G):
     nodes = [64, 43, 22, 21, 1]
     _check(kvq, cuda_dev, bits, 2, G, [70, 300, 5, 0, 129], nodes, seed=50 + G)     # whole units
     _check(kvq, cuda_dev, bits, 2, G, [2600, 300, 1500, 0, 129], nodes, ps=32, seed=60 + G, tail=1)
+
+
+@pytest.mark.parametrize("bits", [8, 6, 4])
+@pytest.mark.parametrize("length", [100, 2500])     # a whole unit, a unit cut over several CTAs
+def test_seen_infinite_values_reach_their_rows_and_channels_only(kvq, cuda_dev, bits, length):
+    c = Cache(kvq, cuda_dev, bits, 1, 16, [length], [30], seed=7)
+    parents = [[-1, 0, 0, 1, 2, -1, 4, 3] + [3] * 22]
+    q_np = kvgen.queries_np(8, 1, 30, 6, D)
+    t = length + 2
+    c.vp[0].scales[int(c.pt_np[0, t // 16]), 0, t % 16] = float("inf")
+    out, err = _call(kvq, cuda_dev, c, dev_tensor(q_np, cuda_dev), parents)
+    assert err == 0
+    out = out[0].double().cpu().numpy()
+    ref, size, span = _reference(c, q_np[0], parents)
+    sees = [i for i in range(30) if i == 2 or op.ancestors(parents[0])[i, 2]]
+    rest = [i for i in range(30) if i not in sees]
+    assert sees == [2, 4, 6]
+    assert_rows_close(out[rest], ref[rest], size[rest], span[rest], "f16")
+    v = c.v_hat[0].reshape(-1, D)[t].astype(np.float64)       # its codes' signs; code 0: 0 * inf
+    want = np.where(v > 0, np.inf, np.where(v < 0, -np.inf, np.nan))
+    for i in sees:
+        for g in range(6):
+            assert np.array_equal(out[i, g], want, equal_nan=True)
