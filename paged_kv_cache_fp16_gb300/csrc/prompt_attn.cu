@@ -488,6 +488,25 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     const int64_t row = (static_cast<int64_t>(n.q0) + tok) * a.Hq + head;
     float* part = a.ws + ((static_cast<int64_t>(blockIdx.x) * a.n_splits + blockIdx.y) * kRows + r) *
                              (D + 4);
+    if (fix && nt > 0) {   // apart from the rows' way out, which short calls run once, from cold
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tc5::ld32(lanes + q * 32, o);
+        tc5::wait_ld32(o);
+        for (int t = max(lim_min, j0 * NB); t < min(limit, j1 * NB); ++t) {
+          const uint16_t* vr = a.v + (n.k0 + t) * a.vs + static_cast<int64_t>(n.h) * D + q * 32;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float v = to_f<BF>(vr[i]);
+            if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+          }
+        }
+        __syncwarp();
+        tc5::st32(lanes + q * 32, o);
+      }
+      tc5::wait_st();
+    }
     const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
     // The rows go through shared memory, over the operands (all products are done), so that they
     // are written whole.  (Stored by each row's thread, 16 bytes here and there: prompts of 128 and
@@ -514,16 +533,6 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       if (!live) continue;
 #pragma unroll
       for (int i = 0; i < 64; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-      if (fix) {
-        for (int t = max(lim_min, j0 * NB); t < min(limit, j1 * NB); ++t) {
-          const uint16_t* vr = a.v + (n.k0 + t) * a.vs + static_cast<int64_t>(n.h) * D + q * 32;
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const float v = to_f<BF>(vr[i]);
-            if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
-          }
-        }
-      }
       if (whole) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
