@@ -100,3 +100,19 @@ def test_captured_and_replayed_on_another_stream(kvq, cuda_dev):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_behind_two_billion_elements(kvq, cuda_dev):
+    n, hq, h, d, stride = 270010, 2, 1, 64, 8192
+    buf = torch.empty((n, stride), dtype=torch.bfloat16, device=cuda_dev)
+    q, k = buf[:, :hq * d].unflatten(1, (hq, d)), buf[:, hq * d:(hq + h) * d].unflatten(1, (h, d))
+    g = torch.Generator().manual_seed(51)
+    buf[:, :(hq + h) * d] = torch.randn((n, 1), generator=g).to(torch.bfloat16).to(cuda_dev)
+    last = torch.randn((64, hq + h, d), generator=g).to(torch.bfloat16).to(cuda_dev)
+    q[-64:], k[-64:] = last[:, :hq], last[:, hq:]
+    phases = kvq.kvq_rope_phases([1.0 / (i + 1) for i in range(d // 2)])
+    pos = torch.arange(n, dtype=torch.int32, device=cuda_dev)
+    qo, ko = last[:, :hq].contiguous(), last[:, hq:].contiguous()
+    kvq.kvq_qk_norm_rope(qo, ko, qo, ko, pos[-64:].contiguous(), phases)
+    kvq.kvq_qk_norm_rope(q, k, q, k, pos, phases)
+    assert torch.equal(q[-64:], qo) and torch.equal(k[-64:], ko)

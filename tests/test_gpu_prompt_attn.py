@@ -254,3 +254,24 @@ def test_lse_of_a_row_of_nan_scores_is_nan(kvq, cuda_dev, keys):
     assert err == 0 and torch.isnan(out[40, 2]).all()
     bad = torch.isnan(lse)
     assert bad[40, 2] and int(bad.sum()) == 1 and torch.isfinite(lse[~bad]).all()
+
+
+def test_rows_behind_two_billion_elements(kvq, cuda_dev):
+    """The same bits as from a small buffer: offsets of q, k, v and out pass 32 bits."""
+    Hq, H, D, at, stride = 6, 1, 128, 270000, 8192
+    new, keys = [40, 1], [40, 90]
+    q, k, v = _inputs(cuda_dev, "f16", new, keys, Hq, H, D, 41)
+    v[60, 0, 3] = float("inf")                       # also the values that are read one by one
+    small, lse, _ = _call(kvq, q, k, v, new, keys, 0.1)
+    buf = torch.empty((at + sum(keys), stride), dtype=torch.float16, device=cuda_dev)
+    rows = lambda lo, x: buf[:at + x.shape[0], lo:lo + x.shape[1] * D].unflatten(1, x.shape[1:])
+    views = []
+    for lo, x in ((0, q), (Hq * D, k), ((Hq + H) * D, v)):
+        w = rows(lo, x)
+        w[at:] = x
+        views.append(w)
+    cu_q, cu_k = [[at + c for c in cu_of(n)] for n in (new, keys)]
+    big, big_lse, err = _call(kvq, *views, new, keys, 0.1, cu_q=cu_q, cu_k=cu_k)
+    assert err == 0
+    assert torch.equal(big[at:].view(torch.int16), small.view(torch.int16))
+    assert torch.equal(big_lse[at:], lse) and (big[:at] == 7).all()

@@ -383,3 +383,29 @@ def test_seen_infinite_values_reach_their_rows_and_channels_only(kvq, cuda_dev, 
     for i in sees:
         for g in range(6):
             assert np.array_equal(out[i, g], want, equal_nan=True)
+
+
+def test_pages_behind_four_billion_bytes(kvq, cuda_dev):
+    """The same bits from small pools and from pools whose pages lie past 2^32 bytes."""
+    c = Cache(kvq, cuda_dev, 8, 4, 16, [150], [9], seed=9)
+    parents = [[-1, 0, 0, 1, 2, 2, 4, -1, 7]]
+    q = dev_tensor(kvgen.queries_np(10, 1, 9, 8, D), cuda_dev)
+    small, err = _call(kvq, cuda_dev, c, q, parents)
+    assert err == 0
+    first = 265000                                     # pages of 16 KB
+    accept, cu = i32([0, 2, 4], cuda_dev), i32([0, 3], cuda_dev)
+    pools = []
+    for p in c.kp + c.vp:
+        b = kvq.Pool.empty(8, 4, D, 16, first + p.codes.shape[0], cuda_dev)
+        b.codes[first:], b.scales[first:] = p.codes, p.scales
+        pools.append(b)
+    small_pools, pt = c.kp + c.vp, c.pt + first
+    c.kp, c.vp = pools[:1], pools[1:]
+    big, err = _call(kvq, cuda_dev, c, q, parents, pt=pt)
+    assert err == 0 and torch.equal(big, small)
+    lens = i32([150], cuda_dev)
+    kvq.kvq_tree_commit(small_pools, c.pt, lens, cu, accept)
+    kvq.kvq_tree_commit(pools, pt, lens, cu, accept)
+    for a, b in zip(small_pools, pools):
+        assert torch.equal(a.codes, b.codes[first:])
+        assert torch.equal(a.scales.view(torch.int16), b.scales[first:].view(torch.int16))
