@@ -3,8 +3,8 @@
 // One thread issues the products; their accumulators, and the A operand of the second product of
 // an attention tile, live in tensor memory (TMEM: 128 lanes x 512 columns of 32 bits per SM).
 // Shared-memory operands are 128-byte rows in the 128-byte swizzle: the 16-byte piece c of row r
-// lies at r * 128 + ((c ^ (r & 7)) * 16), which is how the tensor copies write them and how
-// swz128() addresses them.
+// lies at r * 128 + ((c ^ (r & 7)) * 16), which is how the tensor copies write them and the products
+// read them.
 #pragma once
 
 #include <cstdint>
