@@ -608,7 +608,9 @@ KVQ_API kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64_t 
  *            each row's sum of exponentials, by which results over different keys are joined.
  * workspace  device scratch of at least kvq_prompt_attn_workspace(...) bytes, 16-byte aligned, no
  *            initialisation needed; two calls that may overlap need one each.
- * dev_err    may be NULL; also gets KVQ_DEVERR_TIMEOUT.
+ * dev_err    may be NULL; also gets KVQ_DEVERR_TIMEOUT: a wait inside the kernel ran out, and the
+ *            rows of out and lse that belong to a sequence hold unspecified values.  (No copy or
+ *            product is in flight any more when a block that gave up ends.)
  * All pointers are device memory (not a host view: tiles are read by the tensor copy engine).
  * head_dim 64, 128 or 256; any Hq that is a multiple of H, at most 128 query heads per KV head.
  * Two calls with the same arguments give the same bits.

@@ -102,10 +102,13 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t cols) {
 
 // Bounded wait for a barrier's phase: false when it did not complete within the limit, or when
 // another role of the block has given up (*gave_up).  The drain of copies and products in flight
-// after that uses mbar_wait_bounded.
-constexpr int kPollLimit = 1 << 20;
+// uses mbar_wait_bounded.  A build may define a smaller limit (down to 0: give up at once) to run
+// the way out.
+#ifndef KVQ_TILE_WAIT_LIMIT
+#define KVQ_TILE_WAIT_LIMIT (1 << 20)
+#endif
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const volatile int* gave_up) {
-  for (int i = 0; i < kPollLimit; ++i) {
+  for (int i = 0; i < (KVQ_TILE_WAIT_LIMIT); ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 63) == 63 && *gave_up) return false;
   }

@@ -71,7 +71,7 @@ struct Lay {
   static_assert(kSlot == C::VR * D * 2, "K and V slots are alike");
   static constexpr int kRing = kQ;
   static constexpr int kBars = kRing + C::kSlots * kSlot;
-  static constexpr int kNumBars = 2 * C::kSlots + 3 + 2 * kScores;
+  static constexpr int kNumBars = 2 * C::kSlots + 4 + 2 * kScores;
   static constexpr int kTotal = kBars + kNumBars * 8 + 16;
   static constexpr int kCols = 512 / C::kCtas;
   static_assert(D + kScores * C::NB <= kCols, "TMEM");
@@ -257,7 +257,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
   uint64_t *full = bars, *empty = bars + SL, *qfull = bars + 2 * SL, *odone = qfull + 1,
-           *sfull = odone + 2, *pready = sfull + kScores;
+           *sfull = odone + 2, *pready = sfull + kScores, *drain = pready + kScores;
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_ptr + 1);   // [0] gave up, [1] V
 
@@ -272,6 +272,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     mbar_init(qfull, 1);
     mbar_init(odone, 1);
     mbar_init(odone + 1, 1);
+    mbar_init(drain, 1);
     for (int i = 0; i < kScores; ++i) { mbar_init(sfull + i, 1); mbar_init(pready + i, kSoftmaxThreads / 32); }
     tc5::fence_barrier_init();
     flags[0] = 0;
@@ -338,11 +339,10 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         if (j + 1 < nt) load_k(j + 1);
         if (ok) load_v(j);
       }
-      if (!ok) {   // wait for the copies in flight
-        for (int i = max(0, pos - SL); i < pos; ++i)
-          mbar_wait_bounded(full + i % SL, (i / SL) & 1);
-        mbar_wait_bounded(qfull, 0);
-      }
+      // Whichever role gives up, and whether this one has by then issued everything or not: no copy
+      // is in flight when the block ends.
+      for (int i = max(0, pos - SL); i < pos; ++i) mbar_wait_bounded(full + i % SL, (i / SL) & 1);
+      mbar_wait_bounded(qfull, 0);
     }
   } else if (warp == 4) {
     // ------------------------------------------------------------------- products (one thread)
@@ -393,11 +393,9 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
         if (j + 1 < nt) product_s(j + 1);
         if (ok) product_o(j);
       }
-      if (!ok) {   // what was issued must end before the memory is given back
-        flags[0] = 1;
-        tc5::commit(qfull);
-        mbar_wait_bounded(qfull, 1);
-      }
+      if (!ok) flags[0] = 1;
+      tc5::commit(drain);   // what was issued ends before the memory is given back, as above
+      mbar_wait_bounded(drain, 0);
     }
   } else {
     // ------------------------------------------------------------------ softmax: thread = row

@@ -527,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] = nx[j];
     }
-    if (!ok) {   // wait for the copies in flight
-      for (int i = max(0, it - R); i < it; ++i) mbar_wait_bounded(full + i % R, (i / R) & 1);
-    }
+    // Whichever role gives up, and whether this one has by then issued everything or not: no copy is
+    // in flight when the block ends.
+    for (int i = max(0, it - R); i < it; ++i) mbar_wait_bounded(full + i % R, (i / R) & 1);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products (one thread)
     const uint32_t base = smem_u32(sm);
@@ -577,12 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       it += g.count;
       ++seg;
     }
-    if (!ok) {   // what was issued must end before the memory is given back
-      flags[0] = 1;
-      if (tc5::elect_one()) {
-        tc5::commit(drain);
-        mbar_wait_bounded(drain, 0);
-      }
+    if (!ok) flags[0] = 1;
+    if (tc5::elect_one()) {   // what was issued ends before the memory is given back, as above
+      tc5::commit(drain);
+      mbar_wait_bounded(drain, 0);
     }
   } else if (warp >= kUnpackWarp0) {
     // ------------------------------------------------------------------------------- unpack
