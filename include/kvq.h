@@ -656,6 +656,8 @@ KVQ_API kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_t q
  *            whose page id is out of range are not attended (KVQ_DEVERR_PAGE_RANGE).
  * workspace  kvq_tree_attn_workspace(...) bytes, 16-byte aligned, no initialisation needed; two
  *            calls that may overlap need one each.
+ * dev_err    also gets KVQ_DEVERR_TIMEOUT, as for kvq_prompt_attn: the rows of out that belong to a
+ *            sequence then hold unspecified values.
  * Values of drafts that a node does not see (infinities and NaN too) do not reach it.
  * head_dim 256; page_size a multiple of 16; at most 16 query heads per KV head.  One call's upper
  * bounds may make 2^30 tiles of 64 tokens at most (layers x KV heads x tiles of 128 rows x

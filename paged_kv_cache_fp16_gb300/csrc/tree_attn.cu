@@ -673,9 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       tc5::meet(quad);
       return v;
     };
+    auto node_of_row = [&]() { return (g.u.r * kRows + r) / a.G; };
+    auto has_drafts = [&]() { return (g.u.tile + g.count) * kTile > g.u.q.len; };
+    int met = 0;   // where this warp gave up: its exchanges of the present segment so far
     while (ok && next_segment(a, w, g)) {
       const Seq& q = g.u.q;
-      const int node = (g.u.r * kRows + r) / a.G;
+      const int node = node_of_row();
       const bool live = node < q.n;
       const bool idle = !__any_sync(kFullMask, live);
       const int64_t row = (static_cast<int64_t>(g.u.l) * a.total + q.n0 + node) * a.Hq +
@@ -710,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       if (lane == 0) mbar_arrive(qready);
       // the ancestors, if drafts are among this segment's tokens
       uint64_t seen = 0;
-      const bool drafts = (g.u.tile + g.count) * kTile > q.len;
+      const bool drafts = has_drafts();
       if (drafts) {
         asm volatile("bar.sync 1, 256;" ::: "memory");   // the previous unit's are no longer read
         if (half == 0 && r < q.n) {
@@ -728,7 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       float m = kNegInf, l = 0.f;
       for (int j = 0; j < g.count; ++j, ++it) {
         ok = warp_wait(sfull + (it & 1), (it >> 1) & 1, flags);
-        if (!ok) break;
+        if (!ok) {
+          met = idle ? 0 : j;
+          break;
+        }
         tc5::fence_after();
         if (idle) {   // no row of this warp is used: its weights may be anything
           if (lane == 0) mbar_arrive(pready + (it & 1));
@@ -763,7 +769,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
             if (up) m = x;
             l *= f;
             ok = warp_wait(odone + ((it - 1) & 1), (it - 1) >> 1 & 1, flags);
-            if (!ok) break;
+            if (!ok) {
+              met = j + 1;
+              break;
+            }
             tc5::fence_after();
 #pragma unroll 1
             for (int b = half * 4; b < half * 4 + 4; ++b) {
@@ -789,7 +798,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       }
       if (!ok) break;
       ok = warp_wait(odone + ((it - 1) & 1), (it - 1) >> 1 & 1, flags);
-      if (!ok) break;
+      if (!ok) {
+        met = idle ? 0 : g.count;
+        break;
+      }
       tc5::fence_after();
       l += other(l);
       const bool whole = g.count == q.tiles;
@@ -857,7 +869,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       }
       tc5::fence_before();
     }
-    if (!ok) flags[0] = 1;
+    if (!ok) {
+      // Another warp may have seen the phase complete whose wait ran out here.  It goes on to the
+      // barriers of the walk, which have no limit of their own, until one of its own waits fails:
+      // so a warp that gave up goes on meeting the others there, to the walk's end (every warp
+      // walks the same segments), and waits for nothing else.
+      flags[0] = 1;
+      auto exchanges = [&]() {   // of a segment: one per tile that has rows of this warp, and l's
+        return (__any_sync(kFullMask, node_of_row() < g.u.q.n) ? g.count : 0) + 1;
+      };
+      int owed = exchanges() - met;
+      for (;;) {
+        for (; owed > 0; --owed) other(0.f);
+        if (!next_segment(a, w, g)) break;
+        if (has_drafts()) {
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
+        owed = exchanges();
+      }
+    }
   }
   if (!ok) flags[0] = 1;
   __syncwarp();
