@@ -3,7 +3,7 @@
 // For a tile of 128 query rows and tiles of NB keys:
 //   S = Q K^T            tcgen05.mma, both operands in shared memory, S (float32) in TMEM
 //   p = 2^(S c - m)      one thread per row (c = softmax_scale log2 e), running maximum and sum
-//   O += P V             tcgen05.mma, P (16 bits) from TMEM over the place of S, O in TMEM
+//   O += P V             tcgen05.mma, P (16 bits) and O in TMEM
 // so the scores never leave the SM and a key is read once per tile of rows.
 //
 // Rows: a tile packs the G = Hq / H query heads of a KV head beside as many tokens as fit
@@ -14,8 +14,14 @@
 // pieces along the channels, a V tile as pieces along its keys, each of which is handed back when
 // its products are done.
 //
-// Per head dimension: at 256, O and two score buffers of 128 keys fill TMEM, one CTA per SM, and
-// the softmax of one tile runs under the products of the next; at 128 and 64 two CTAs share an SM
+// TMEM holds O, one score buffer (two at 64 channels) and two of weights.  Scores are formed over
+// scores that the softmax has in registers, and weights are written over those of the product before
+// last: every reuse follows a barrier, because only products of one shape and accumulator are
+// promised to run in the order of their issue.  (Two score buffers with the weights over the scores,
+// and a wait for the product that reads them before the next scores: 512 queries over 16,500 keys at
+// 256 channels 168 us, this way 154; at 64 and 128 channels equal.)
+// Per head dimension: at 256, O, S and P of 128 keys fill TMEM, one CTA per SM, and the softmax of
+// one tile runs under the products of the next; at 128 and 64 two CTAs share an SM
 // and cover each other's softmax.  What bounds it (one GB300, whole prompts of 16,384 tokens): at
 // 256 the tensor cores (1,690 to 1,815 TFLOP/s in fp16, 1,740 to 1,900 in bf16, by the chip's
 // power); at 128 the tensor cores fed from shared memory (a product of 128 x 64 x 16 with both
@@ -51,17 +57,22 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kSoftmaxThreads = 128;
 constexpr int kThreads = 192;
-constexpr int kScores = 2;   // score buffers
 
 // NB: keys per tile.  KD: channels of a K slot (NB rows).  VR: keys of a V slot (D channels).
-// kSlots: ring slots.  kCtas: resident CTAs per SM.  Two score buffers each.
+// kSlots: ring slots.  kCtas: resident CTAs per SM.  kScores: score buffers.
 // Measured against each other (16,384 tokens, TFLOP/s): at 128 channels one buffer of 128 keys
 // 1,049, two of 64 1,354; at 64 channels two of 64 in 2 CTAs 972, one of 128 in 2 CTAs 790, two of
-// 128 in 1 CTA 749, one of 64 in 4 CTAs 848; three buffers of 64 as fast as two.
+// 128 in 1 CTA 749, one of 64 in 4 CTAs 848 (buffers then held the weights too).
 template <int D> struct Cfg;
-template <> struct Cfg<256> { static constexpr int NB = 128, KD = 128, VR = 64, kSlots = 5, kCtas = 1; };
-template <> struct Cfg<128> { static constexpr int NB = 64, KD = 128, VR = 64, kSlots = 5, kCtas = 2; };
-template <> struct Cfg<64> { static constexpr int NB = 64, KD = 64, VR = 64, kSlots = 8, kCtas = 2; };
+template <> struct Cfg<256> {
+  static constexpr int NB = 128, KD = 128, VR = 64, kSlots = 5, kCtas = 1, kScores = 1;
+};
+template <> struct Cfg<128> {
+  static constexpr int NB = 64, KD = 128, VR = 64, kSlots = 5, kCtas = 2, kScores = 1;
+};
+template <> struct Cfg<64> {
+  static constexpr int NB = 64, KD = 64, VR = 64, kSlots = 8, kCtas = 2, kScores = 2;
+};
 
 template <int D>
 struct Lay {
@@ -71,10 +82,11 @@ struct Lay {
   static_assert(kSlot == C::VR * D * 2, "K and V slots are alike");
   static constexpr int kRing = kQ;
   static constexpr int kBars = kRing + C::kSlots * kSlot;
-  static constexpr int kNumBars = 2 * C::kSlots + 4 + 2 * kScores;
+  static constexpr int kNumBars = 2 * C::kSlots + 9;
   static constexpr int kTotal = kBars + kNumBars * 8 + 16;
   static constexpr int kCols = 512 / C::kCtas;
-  static_assert(D + kScores * C::NB <= kCols, "TMEM");
+  static constexpr int kS = D, kP = D + C::kScores * C::NB;   // TMEM columns: O at 0, S, two of P
+  static_assert(kP + 2 * (C::NB / 2) <= kCols, "TMEM");
   static_assert(kRows * D * 4 <= kBars, "the results are staged over the operands");
   static constexpr int nk = D / C::KD, nv = C::NB / C::VR;
 };
@@ -257,7 +269,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::kBars);
   uint64_t *full = bars, *empty = bars + SL, *qfull = bars + 2 * SL, *odone = qfull + 1,
-           *sfull = odone + 2, *pready = sfull + kScores, *drain = pready + kScores;
+           *sfull = odone + 2, *sfree = sfull + 2, *pready = sfree + 1, *drain = pready + 2;
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* flags = reinterpret_cast<volatile int*>(tmem_ptr + 1);   // [0] gave up, [1] V
 
@@ -273,7 +285,11 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
     mbar_init(odone, 1);
     mbar_init(odone + 1, 1);
     mbar_init(drain, 1);
-    for (int i = 0; i < kScores; ++i) { mbar_init(sfull + i, 1); mbar_init(pready + i, kSoftmaxThreads / 32); }
+    mbar_init(sfull, 1);
+    mbar_init(sfull + 1, 1);
+    mbar_init(sfree, kSoftmaxThreads / 32);
+    mbar_init(pready, kSoftmaxThreads / 32);
+    mbar_init(pready + 1, kSoftmaxThreads / 32);
     tc5::fence_barrier_init();
     flags[0] = 0;
     flags[1] = 0;
@@ -353,27 +369,30 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       int pos = 0;
       bool ok = tc5::wait(qfull, 0, flags);
       auto product_s = [&](int j) {
-        const uint32_t d = tmem + D + (j & 1) * NB;
         for (int i = 0; i < L::nk; ++i, ++pos) {
           ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);
+          if (C::kScores == 1 && i == 0 && j > 0) {   // (of two, tile j - 2's: pready told)
+            ok = ok && tc5::wait(sfree, (j - 1) & 1, flags);
+            tc5::fence_after();
+          }
           if (!ok) return;
           const uint32_t kb = ring + (pos % SL) * L::kSlot;
 #pragma unroll
           for (int k = 0; k < C::KD / 16; ++k) {
             const int kq = i * (C::KD / 16) + k;   // the contraction step within the row
-            tc5::mma_ss(d, tc5::desc_at(dk, base + (kq / 4) * kRows * 128 + (kq % 4) * 32),
+            tc5::mma_ss(tmem + L::kS + j % C::kScores * NB, tc5::desc_at(dk, base + (kq / 4) * kRows * 128 + (kq % 4) * 32),
                         tc5::desc_at(dk, kb + (k / 4) * NB * 128 + (k % 4) * 32), id_s, kq > 0);
           }
           tc5::commit(empty + pos % SL);
         }
-        tc5::commit(sfull + (j & 1));
+        tc5::commit(sfull + (j & 1));   // completes when everything issued before has: O of tile j - 2 too
       };
       auto product_o = [&](int j) {
         ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);   // sooner than the weights
         ok = ok && tc5::wait(pready + (j & 1), (j >> 1) & 1, flags);
         if (!ok) return;
         tc5::fence_after();
-        const uint32_t pb = tmem + D + (j & 1) * NB;
+        const uint32_t pb = tmem + L::kP + (j & 1) * (NB / 2);
         for (int i = 0; i < L::nv; ++i, ++pos) {
           if (i > 0) ok = ok && tc5::wait(full + pos % SL, (pos / SL) & 1, flags);
           if (!ok) return;
@@ -388,8 +407,6 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       };
       if (ok) product_s(0);
       for (int j = 0; j < nt && ok; ++j) {
-        // the next scores go over the weights of tile j - 1, whose product was issued before:
-        // products of one CTA run in the order of their issue
         if (j + 1 < nt) product_s(j + 1);
         if (ok) product_o(j);
       }
@@ -410,13 +427,12 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       ok = warp_wait(sfull + (j & 1), (j >> 1) & 1, flags);
       if (!ok) break;
       tc5::fence_after();
-      const uint32_t sb = lanes + D + (j & 1) * NB;
       const int t0 = (j0 + j) * NB;
       const bool edge = t0 + NB > lim_min;
       const int left = limit - t0;   // columns that the row sees
       uint32_t s[NB];
 #pragma unroll
-      for (int q = 0; q < NB / 32; ++q) tc5::ld32(sb + q * 32, s + q * 32);
+      for (int q = 0; q < NB / 32; ++q) tc5::ld32(lanes + L::kS + j % C::kScores * NB + q * 32, s + q * 32);
       tc5::wait_ld32(s);
 #pragma unroll
       for (int q = 1; q < NB / 32; ++q) tc5::after_ld32(s + q * 32);
@@ -426,6 +442,11 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
           if (i >= left) s[i] = 0xff800000u;
       }
       const float x = tc5::row_max<NB>(s) * a.c;
+      if constexpr (C::kScores == 1) {   // the next scores may come (said before the maximum: 1 % slower)
+        tc5::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sfree);
+      }
       if (j == 0) {
         m = x;
       } else {
@@ -452,8 +473,8 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
       const float mo = m == kNegInf ? 0.f : m - tc5::kOff;
       uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int q = 0; q < NB / 32; ++q) {   // over the scores already read
-        tc5::weights32<BF>(s + q * 32, a.c, mo, sb + q * 16, sum);
+      for (int q = 0; q < NB / 32; ++q) {   // over the weights of tile j - 2: sfull told of their product
+        tc5::weights32<BF>(s + q * 32, a.c, mo, lanes + L::kP + (j & 1) * (NB / 2) + q * 16, sum);
       }
       l += tc5::sum_of(sum);
       tc5::wait_st();

@@ -540,6 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
       if (tc5::elect_one()) {
         auto product_s = [&](int i) {
           ok = ok && tc5::wait(kfull + (i & 1), (i >> 1) & 1, flags);
+          // These scores go over the weights of tile i - 2, once their product is done: only products
+          // of one shape and accumulator are promised to run in the order of their issue.  (The first
+          // two tiles of a segment follow on qready, before which all products were done.)
+          if (i >= it + 2) ok = ok && tc5::wait(odone + (i & 1), (i - 2) >> 1 & 1, flags);
           if (!ok) return;
           tc5::fence_after();
           const uint32_t kb = base + L::kK + (i & 1) * kStage;
@@ -567,8 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
         tc5::fence_after();
         if (ok) product_s(it);
         for (int j = 0; ok && j < g.count; ++j) {
-          // the next scores go over the weights of the tile before this one, whose product was
-          // issued earlier: products of one CTA run in the order of their issue
           if (j + 1 < g.count) product_s(it + j + 1);
           if (ok) product_o(it + j, j == 0);
         }
