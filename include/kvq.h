@@ -607,7 +607,9 @@ KVQ_API kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64_t 
  * out        `dtype` [total_q][Hq][D]; lse float32 [total_q][Hq] or NULL: the natural logarithm of
  *            each row's sum of exponentials, by which results over different keys are joined.
  * workspace  device scratch of at least kvq_prompt_attn_workspace(...) bytes, 16-byte aligned, no
- *            initialisation needed; two calls that may overlap need one each.
+ *            initialisation needed; two calls that may overlap need one each.  The size for some
+ *            nseq, total_q, max_q and max_k suffices for every call of the same heads and head_dim
+ *            with none of the four larger (20.6 MB at most).
  * dev_err    may be NULL; also gets KVQ_DEVERR_TIMEOUT: a wait inside the kernel ran out, and the
  *            rows of out and lse that belong to a sequence hold unspecified values.  (No copy or
  *            product is in flight any more when a block that gave up ends.)

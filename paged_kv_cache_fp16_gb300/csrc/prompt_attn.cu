@@ -700,6 +700,7 @@ prompt_join_kernel(const __grid_constant__ PromptArgs a) {
 struct Plan {
   int tpt, tps, n_splits;
   int64_t units;
+  int64_t most_parts;   // units x splits of this call and of any with smaller bounds, if more than one split
 };
 
 Plan plan_for(int nseq, int total_q, int num_q_heads, int num_kv_heads, int D, int max_q,
@@ -716,12 +717,20 @@ Plan plan_for(int nseq, int total_q, int num_q_heads, int num_kv_heads, int D, i
   // its start (about the time of two tiles) and its partial rows.
   int64_t want = p.units > 0 ? slots / p.units : 1;
   const int64_t most = (tiles + 3) / 4;
+  // n_splits is at most `want`, so units * n_splits at most slots, and at most units * most; both
+  // bounds fall with each of the call's
+  p.most_parts = most <= 1 ? 0 : (p.units < slots / most ? p.units * most : slots);
   want = want > most ? most : want;
   if (want < 1) want = 1;
   p.tps = static_cast<int>((tiles + want - 1) / want);
   if (p.tps < 1) p.tps = 1;
   p.n_splits = tiles > 0 ? static_cast<int>((tiles + p.tps - 1) / p.tps) : 1;
   return p;
+}
+
+// Partial rows: O, m, l and two floats of padding, 128 rows of each part.
+size_t parts_bytes(int64_t parts, int D) {
+  return static_cast<size_t>(parts) * kRows * (D + 4) * sizeof(float);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -807,8 +816,7 @@ extern "C" size_t kvq_prompt_attn_workspace(int nseq, int total_q, int num_q_hea
     return 0;
   const kvq::Plan p =
       kvq::plan_for(nseq, total_q, num_q_heads, num_kv_heads, head_dim, max_q, max_k);
-  if (p.n_splits == 1) return 16;
-  return static_cast<size_t>(p.units) * p.n_splits * kvq::kRows * (head_dim + 4) * sizeof(float);
+  return p.most_parts ? kvq::parts_bytes(p.most_parts, head_dim) : 16;
 }
 
 extern "C" kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_t q_stride,
@@ -849,11 +857,10 @@ extern "C" kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
       !aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u))
     return fail(KVQ_ERR_ALIGN, "%s: a pointer is not 16-byte aligned (lse 4)", fn);
-  const size_t need = kvq_prompt_attn_workspace(nseq, total_q, num_q_heads, num_kv_heads,
-                                                head_dim, max_q, max_k);
+  const Plan p = plan_for(nseq, total_q, num_q_heads, num_kv_heads, head_dim, max_q, max_k);
+  const size_t need = p.n_splits == 1 ? 16 : parts_bytes(p.units * p.n_splits, head_dim);
   if (workspace_bytes < need)
     return fail(KVQ_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", fn, workspace_bytes, need);
-  const Plan p = plan_for(nseq, total_q, num_q_heads, num_kv_heads, head_dim, max_q, max_k);
   if (p.units > INT32_MAX)
     return fail(KVQ_ERR_RANGE, "%s: %lld row tiles exceed the grid", fn,
                 static_cast<long long>(p.units));
