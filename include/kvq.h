@@ -654,7 +654,9 @@ KVQ_API kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_t q
  *            [total_nodes].
  * max_nodes  host upper bound on a sequence's drafts, in [1, KVQ_MAX_NODES]; max_seq_len host
  *            upper bound on seq_lens[s] plus its drafts.  A sequence that exceeds them is skipped
- *            (KVQ_DEVERR_INDEX); a parent outside [-1, i) counts as -1 (KVQ_DEVERR_INDEX).  Tokens
+ *            (KVQ_DEVERR_INDEX), and all of them are if offsets that fall give the same drafts to more
+ *            sequences than the bounds have row tiles for; a parent outside [-1, i) counts as -1
+ *            (KVQ_DEVERR_INDEX).  Tokens
  *            whose page id is out of range are not attended (KVQ_DEVERR_PAGE_RANGE).
  * workspace  kvq_tree_attn_workspace(...) bytes, 16-byte aligned, no initialisation needed; two
  *            calls that may overlap need one each.

@@ -91,6 +91,7 @@ struct TreeArgs {
   int n_layers, nseq, total, H, Hq, G, ps, max_pages, max_nodes, max_len;
   int grid;     // CTAs of the attention kernel
   int whole;    // deal whole units (short caches)
+  uint32_t most_units, most_tiles;   // of a layer, by the call's bounds
   Cut* cuts;    // [grid]
   float c;      // softmax_scale * log2(e)
 };
@@ -157,18 +158,30 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t x) {
   return x;
 }
 
-// Tiles and units of one layer (whole warp).  The call's tiles fit 31 bits.
+__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {   // of sums below 2^51
+  const uint64_t hi = __reduce_add_sync(kFullMask, static_cast<uint32_t>(x >> 24));
+  return (hi << 24) + __reduce_add_sync(kFullMask, static_cast<uint32_t>(x) & 0xffffffu);
+}
+
+// Tiles and units of one layer (whole warp).  The call's fit 31 bits.  Offsets that fall and rise
+// again can give the same drafts to many sequences, up to eight times (below 2^33) what the bounds
+// allow and the line of tiles is numbered for: such a call is given no work.
 __device__ __forceinline__ void layer_totals(const TreeArgs& a, bool check, uint32_t& tiles,
                                              uint32_t& units) {
   const int lane = threadIdx.x & 31;
-  uint32_t t = 0, u = 0;
+  uint64_t t = 0, u = 0;
   for (int s = lane; s < a.nseq; s += 32) {
     const Seq q = seq_of(a, s, check);
-    u += static_cast<uint32_t>(q.rt) * a.H;
-    t += static_cast<uint32_t>(q.rt) * a.H * q.tiles;
+    const uint64_t mine = static_cast<uint64_t>(q.rt) * a.H;
+    u += mine;
+    t += mine * q.tiles;
   }
-  tiles = __reduce_add_sync(kFullMask, t);
-  units = __reduce_add_sync(kFullMask, u);
+  t = warp_sum(t);
+  u = warp_sum(u);
+  const bool bad = u > a.most_units || t > a.most_tiles;
+  if (bad && check) report(a.err, KVQ_DEVERR_INDEX);
+  tiles = bad ? 0 : static_cast<uint32_t>(t);
+  units = bad ? 0 : static_cast<uint32_t>(u);
 }
 
 struct Unit {
@@ -1099,6 +1112,8 @@ extern "C" kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_p
   a.n_layers = n_layers; a.nseq = nseq; a.total = total_nodes; a.H = H; a.Hq = num_q_heads;
   a.G = num_q_heads / H; a.ps = k0.page_size; a.max_pages = max_pages; a.max_nodes = max_nodes;
   a.max_len = max_seq_len; a.grid = p.grid; a.whole = p.whole ? 1 : 0;
+  a.most_units = static_cast<uint32_t>(p.units / n_layers);
+  a.most_tiles = static_cast<uint32_t>(p.units / n_layers * seq_tiles);
   a.cuts = reinterpret_cast<Cut*>(a.ws + static_cast<int64_t>(p.grid) * 2 * kRec);
   a.c = c;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
