@@ -832,8 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attn_kernel(const __grid_con
           const int hi = min(q.n, (g.u.tile + g.count) * kTile - q.len);
           for (int d = lo; d < hi; ++d) {
             if (!(seen >> d & 1)) continue;
-            const int64_t at = locate_row(a.pt, a.max_pages, a.ps, a.H, P.v_pages, g.u.s,
-                                          static_cast<int64_t>(q.len) + d, g.u.h, nullptr);
+            const int64_t at =   // (a page that only one of K and V has is not attended)
+                locate_row(a.pt, a.max_pages, a.ps, a.H, min(P.k_pages, P.v_pages), g.u.s,
+                           static_cast<int64_t>(q.len) + d, g.u.h, nullptr);
             if (at < 0) continue;
             const float vs = h2f(P.vs[at]);
 #pragma unroll
