@@ -82,3 +82,20 @@ def test_drafts_on_a_page_that_one_pool_lacks_are_not_attended(kvq, cuda_dev, fe
         ref, _, size, span = op.attend(q_np[0, rows, g], c.k_hat[0][:keep, 0], c.v_hat[0][:keep, 0],
                                        seen[rows], 1 / 16)
         assert_rows_close(out[0, rows, g].double().cpu().numpy(), ref, size, span, "f16")
+
+
+@pytest.mark.parametrize("bits", [8, 6, 4])
+def test_a_long_cache(kvq, cuda_dev, bits):
+    length, nodes, G = 131000, 5, 6
+    c = Cache(kvq, cuda_dev, bits, 1, 16, [length], [nodes], seed=bits)
+    parents = [-1, 0, 0, 1, 2]
+    q_np = kvgen.queries_np(bits, 1, nodes, G, D)
+    q = dev_tensor(q_np, cuda_dev)
+    out, err = torch.full_like(q, 7.0), i32([0], cuda_dev)
+    ws = kvq.tree_workspace(c.kp, 1, nodes, G, nodes, length + nodes, cuda_dev)
+    kvq.kvq_tree_attn(c.kp, c.vp, q, c.pt, i32([length], cuda_dev), i32([0, nodes], cuda_dev),
+                      i32(parents, cuda_dev), nodes, length + nodes, 1 / 16, out, ws, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    ref, size, span = op.tree_attention(q_np[0], c.k_hat[0], c.v_hat[0], length, parents, 1 / 16)
+    assert_rows_close(out[0].double().cpu().numpy(), ref, size, span, "f16")
