@@ -615,7 +615,8 @@ KVQ_API kvq_status kvq_qk_norm_rope(kvq_dtype dtype, const uint16_t* q, int64_t 
  *            product is in flight any more when a block that gave up ends.)
  * All pointers are device memory (not a host view: tiles are read by the tensor copy engine).
  * head_dim 64, 128 or 256; any Hq that is a multiple of H, at most 128 query heads per KV head.
- * Two calls with the same arguments give the same bits.
+ * Two calls with the same arguments give the same bits.  A weight below 2^-35 of its row's largest
+ * may be rounded to 0, so that an infinite value that a row sees with such a weight gives NaN.
  * Errors: KVQ_ERR_SHAPE (dtype, heads, head_dim, strides), KVQ_ERR_NULL, KVQ_ERR_ALIGN,
  * KVQ_ERR_RANGE (counts, total_k above 2^31 - 129, more than 2^31 - 1 tiles of 128 rows;
  * softmax_scale not in (0, 2.3e38]), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
@@ -663,7 +664,8 @@ KVQ_API kvq_status kvq_prompt_attn(kvq_dtype dtype, const uint16_t* q, int64_t q
  * dev_err    also gets KVQ_DEVERR_TIMEOUT, as for kvq_prompt_attn: the rows of out that belong to a
  *            sequence then hold unspecified values.
  * Values of drafts that a node does not see (infinities and NaN too) do not reach it.
- * head_dim 256; page_size a multiple of 16; at most 16 query heads per KV head.  One call's upper
+ * head_dim 256; page_size a multiple of 16; at most 16 query heads per KV head; the plain pages only
+ * (not those with sinks and outliers of kvq_decode_attn_side, nor packed KIVI).  One call's upper
  * bounds may make 2^30 tiles of 64 tokens at most (layers x KV heads x tiles of 128 rows x
  * max_seq_len / 64), and max_seq_len may be 2^31 - 65.
  * Errors: KVQ_ERR_SHAPE, KVQ_ERR_BITS, KVQ_ERR_NULL, KVQ_ERR_ALIGN, KVQ_ERR_RANGE (also
@@ -687,7 +689,8 @@ KVQ_API kvq_status kvq_tree_attn(const kvq_pool* k_pools, const kvq_pool* v_pool
  * seq_lens[s] + i.  All of a sequence's rows are read before any is written, so any order of node
  * numbers, repeated ones too, is fine.  seq_lens is not advanced: the caller adds the count.
  * pools      host array [n_tensors] (all with the same bits, num_heads, head_dim, page_size): the
- *            K and V pools of every layer.
+ *            K and V pools of every layer, each once; no two sequences may share the pages that hold
+ *            the drafts.
  * cu_accept  device int32 [nseq+1], non-decreasing, at most total_accept; accept device int32
  *            [total_accept], node numbers in [0, KVQ_MAX_NODES).  A sequence with more than
  *            KVQ_MAX_NODES of them, or offsets out of range, is skipped, and a row whose node

@@ -201,8 +201,9 @@ __device__ __forceinline__ void rows_of(const Lane& L, const NormRopeArgs& a, co
   else rows<BF, LPR, INTER, false>(L, a, x, y, own, part, n, n_max, v);
 }
 
-// 64 registers and 32 warps per SM: loads in flight and other warps' arithmetic cover each other.
-// 32,768 tokens: 155 us, 6.05 TB/s (24 warps 162 us, 40 warps, which spill, 238 us).
+// 64 registers (and 68 to 92 bytes of spills) and 32 warps per SM: loads in flight and other warps'
+// arithmetic cover each other.  32,768 tokens: 155 us, 6.05 TB/s (24 warps 162 us; 40 warps, which
+// spill far more, 238 us).
 template <bool BF, int LPR, bool INTER>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) norm_rope_kernel(const NormRopeArgs a) {
   Lane L;

@@ -21,13 +21,14 @@
 // and a wait for the product that reads them before the next scores: 512 queries over 16,500 keys at
 // 256 channels 168 us, this way 154; at 64 and 128 channels equal.)
 // Per head dimension: at 256, O, S and P of 128 keys fill TMEM, one CTA per SM, and the softmax of
-// one tile runs under the products of the next; at 128 and 64 two CTAs share an SM
-// and cover each other's softmax.  What bounds it (one GB300, whole prompts of 16,384 tokens): at
-// 256 the tensor cores (1,690 to 1,815 TFLOP/s in fp16, 1,740 to 1,900 in bf16, by the chip's
-// power); at 128 the tensor cores fed from shared memory (a product of 128 x 64 x 16 with both
-// operands there takes 48 cycles, not 32; 1,300 to 1,450 TFLOP/s); at 64 the softmax's chain of
-// waits, exponentials and stores, 1,340 cycles per tile and CTA (850 to 990 TFLOP/s, tensor and
-// exponential units 35-40 % busy).  One token over 131,000 keys at 256 channels: 86 us, 6.26 TB/s.
+// one tile runs under the products of the next; at 128 and 64 two CTAs share an SM and cover each
+// other's softmax.  What bounds it (one GB300, whole prompts of 16,384 tokens in short runs): at 256
+// the tensor cores (1,730 to 1,760 TFLOP/s in fp16, 1,790 to 1,840 in bf16, by the chip's power;
+// 1,490 to 1,520 in long runs); at 128 the tensor cores fed from shared memory (a product of 128 x 64
+// x 16 with both operands there takes 48 cycles, not 32; 1,380 to 1,480 TFLOP/s); at 64 the
+// softmax's chain of waits, exponentials and stores, 1,340 cycles per tile and CTA (860 to 960
+// TFLOP/s, tensor and exponential units 35 % busy).  One token over 131,000 keys at 256 channels:
+// 86.5 us, 6.2 TB/s.
 //
 // Keys that a row does not see: scores are set to -inf whatever they hold; in the tiles where some
 // row's view ends, V rows that no row sees are zeroed and non-finite V values that only some rows
@@ -380,7 +381,8 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
 #pragma unroll
           for (int k = 0; k < C::KD / 16; ++k) {
             const int kq = i * (C::KD / 16) + k;   // the contraction step within the row
-            tc5::mma_ss(tmem + L::kS + j % C::kScores * NB, tc5::desc_at(dk, base + (kq / 4) * kRows * 128 + (kq % 4) * 32),
+            tc5::mma_ss(tmem + L::kS + j % C::kScores * NB,
+                        tc5::desc_at(dk, base + (kq / 4) * kRows * 128 + (kq % 4) * 32),
                         tc5::desc_at(dk, kb + (k / 4) * NB * 128 + (k % 4) * 32), id_s, kq > 0);
           }
           tc5::commit(empty + pos % SL);
@@ -442,7 +444,7 @@ prompt_attn_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__
           if (i >= left) s[i] = 0xff800000u;
       }
       const float x = tc5::row_max<NB>(s) * a.c;
-      if constexpr (C::kScores == 1) {   // the next scores may come (said before the maximum: 1 % slower)
+      if constexpr (C::kScores == 1) {   // the next scores may come (said before the maximum: slower)
         tc5::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sfree);
@@ -700,7 +702,7 @@ prompt_join_kernel(const __grid_constant__ PromptArgs a) {
 struct Plan {
   int tpt, tps, n_splits;
   int64_t units;
-  int64_t most_parts;   // units x splits of this call and of any with smaller bounds, if more than one split
+  int64_t most_parts;   // units x splits at most, of this call and any with smaller bounds; 0: never split
 };
 
 Plan plan_for(int nseq, int total_q, int num_q_heads, int num_kv_heads, int D, int max_q,

@@ -19,12 +19,13 @@
 // What bounds it: per tile of 64 tokens shared memory moves 178 KB at q6 (codes in and out, K_hat
 // and V_hat in and out: 1,390 cycles), the unpacking and the softmax issue 5,300 warp instructions
 // (1,340 cycles of the four schedulers), the products take 1,024 and the codes' arrival 1,060; they
-// overlap to 2,450 cycles, the unpacking warps being busy for 2,000 of them (reads, arithmetic and
+// overlap to 2,500 cycles, the unpacking warps being busy for 2,000 of them (reads, arithmetic and
 // the waits for the double buffers, which fill shared memory).  262,000 tokens and 16 drafts of 6
-// heads: q6 138 us (2.95 TB/s, 746 TFLOP/s), q4 129 us; 8 x 20,000 tokens q8, 10 drafts 98 us
-// (3.4 TB/s), 64 drafts (3 row tiles) 268 us.  Measured against this: 16 unpacking warps (fewer
-// registers each) and 4 softmax warps slower; two copying warps for each of K and V leave 80
-// registers, 158 us.
+// heads: q6 142 us (2.87 TB/s, 726 TFLOP/s), q4 130 us; 8 x 20,000 tokens q8, 10 drafts 100 us
+// (3.3 TB/s), 64 drafts (3 row tiles) 273 us.  The 96 registers that 19 warps leave are not quite
+// enough (84 to 88 bytes of spills).  Measured against this: 16 unpacking warps (fewer registers
+// each) and 4 softmax warps slower; two copying warps for each of K and V leave 80 registers, 158 us;
+// a thread each for the two products, 8 ragged caches with 64 drafts at q8 214 instead of 189 us.
 //
 // Work: the tiles of all (layer, sequence, KV head, row tile) units in one line are dealt to the
 // CTAs in equal contiguous shares, whatever the sequences' lengths (which only the device knows).
@@ -278,8 +279,8 @@ __device__ __forceinline__ bool next_segment(const TreeArgs& a, Walk& w, Segment
 }
 
 // The constants of the unpacking, read from shared memory into registers once per warp: spelt out
-// in the code, the compiler sets them anew at most uses (an instruction takes one immediate), which
-// was a quarter of all instructions.
+// in the code, the compiler sets them anew at most uses (an instruction takes one immediate): 6,219
+// warp instructions per tile instead of 5,344.
 template <int BITS> __device__ __forceinline__ constexpr uint32_t unpack_constant(int i) {
   if (BITS == 8) return i == 0 ? 0x80808080u : i == 1 ? 0x64646464u : kHm1152;
   if (BITS == 6)
