@@ -141,14 +141,6 @@ def _layout(case):
     return table, used
 
 
-def _pool_pages(case, used):
-    """Pages of the pools: those in use and what is spare, at least what an update's calls may need."""
-    spare = int(used * case.get("spare", 0)) + 8
-    if case["op"] == "update":
-        spare = max(spare, case["groups"] * case["beams"] * (_pages(case["room"]) + 1))
-    return used + spare
-
-
 def _packed_dim(case):
     return case["dim"] * case.get("bits", 4) // 8
 
@@ -172,7 +164,7 @@ def work(case):
                 + 4 * sum(_pages(n) * b for n in length),
                 "flops": 4 * case["layers"] * case["dim"] * hq * b * sum(length)}
     table, used = _layout(case)
-    pages = _pool_pages(case, used)
+    pages = used + int(used * case["spare"]) + 8
     entries = sum(_pages(n) * b for n in length)
     if case["op"] == "compact":
         moved = used * (pages - used) // pages
@@ -237,7 +229,7 @@ def prepare(case, seed):
     prompt, length = _lens(case)
     b, dim = case["beams"], case["dim"]
     hq, h = HEADS[dim]
-    pages = _pool_pages(case, used)
+    pages = used + int(used * case.get("spare", 0)) + 8
     place = torch.randperm(pages, generator=host).to(torch.int32)
     table = torch.where(table >= 0, place[table.clamp(min=0).long()], -1)
     lens = torch.tensor(length, dtype=torch.int32).repeat_interleave(b)
