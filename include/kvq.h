@@ -780,7 +780,8 @@ KVQ_API kvq_status kvq_beam_select(kvq_dtype dtype, const void* logits, int64_t 
  *            other or max_pages counts as empty (its pages keep their owners), a parent out of range as
  *            -1, a room that is negative or does not fit as 0, counts below 0 are found.
  *            KVQ_DEVERR_PAGE_RANGE: an entry out of range is passed on and counted nowhere.
- *            KVQ_DEVERR_TIMEOUT: the blocks did not meet; the outputs are unspecified.
+ *            KVQ_DEVERR_TIMEOUT: the blocks did not meet; the outputs are unspecified, the inputs and the
+ *            pools as they were.
  * Errors: those of kvq_quant_pack_paged, KVQ_ERR_SHAPE (num_pages differ), KVQ_ERR_RANGE (more than
  * KVQ_MAX_TABLE_SEQS sequences; an output that is its input), KVQ_ERR_WORKSPACE.
  */

@@ -53,7 +53,7 @@ struct TableArgs {
   const int32_t *table, *lens, *held, *refs, *parents, *room;
   int32_t *table_out, *lens_out, *held_out, *refs_out, *live_out;
   int32_t* err;
-  int32_t* bar;                        // grid barrier: arrivals
+  int32_t* bar;                        // a grid's plan: arrivals, blocks that gave up waiting; NULL for other plans
   int32_t* blk;                        // free (update) or used (compact) pages per block
   int32_t *place, *from;               // compact: place of rank i, page of rank i
   int32_t* rank;                       // compact: per page
@@ -88,8 +88,15 @@ struct ClusterMeet {
   }
 };
 
+// Polls of a meeting before a block gives up; a build may define a smaller limit (down to 0: give up at
+// once) to run that path.
+#ifndef KVQ_MEET_WAIT_LIMIT
+#define KVQ_MEET_WAIT_LIMIT (1LL << 22)
+#endif
+
 // A cooperative grid: arrivals counted in global memory (zeroed before the launch), with a bounded
-// wait.  A block that gave up tells the others by leaving them to their own limits, and reports it.
+// wait.  A block that gave up leaves the others to their own limits, reports it and is counted: the blocks
+// that met after all do not know of it, so the moves ask whether there was one.
 struct GridMeet {
   int32_t* bar;
   int32_t* err;
@@ -103,12 +110,15 @@ struct GridMeet {
     if (threadIdx.x == 0) {
       atomicAdd(bar, 1);
       met = false;
-      for (long long i = 0; i < kWaitLimit && !met; ++i) {
+      for (long long i = 0; i < static_cast<long long>(KVQ_MEET_WAIT_LIMIT) && !met; ++i) {
         int v;
         asm volatile("ld.acquire.gpu.s32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
         met = v >= goal;
       }
-      if (!met) report(err, KVQ_DEVERR_TIMEOUT);
+      if (!met) {
+        atomicAdd(bar + 1, 1);
+        report(err, KVQ_DEVERR_TIMEOUT);
+      }
       __threadfence();
     }
     return __syncthreads_and(met);
@@ -118,6 +128,9 @@ struct GridMeet {
 // Data that this launch writes and reads back goes through L2.
 __device__ __forceinline__ int ld(const int32_t* p) { return __ldcg(p); }
 __device__ __forceinline__ void st(int32_t* p, int v) { __stcg(p, v); }
+
+// Whether a block of the plan gave up: then what it had to write holds anything, and nothing is moved.
+__device__ __forceinline__ bool gave_up(const TableArgs& a) { return a.bar && ld(a.bar + 1) != 0; }
 
 // Sum over the block; every thread gets it.
 __device__ __forceinline__ int block_sum(int v, int* sm) {
@@ -256,7 +269,6 @@ __device__ __forceinline__ void update_body(const TableArgs& a) {
   const int n_cta = gridDim.x, cta = blockIdx.x, tid = threadIdx.x;
   const int all = n_cta * kThreads, me = cta * kThreads + tid;
 
-  if (me == 0) a.count[0] = 0;           // nothing to move unless the plan comes to its end
   for (int i = me; i < a.num_pages; i += all) st(a.refs_out + i, __ldg(a.refs + i));
   for (int i = tid; i < a.n_in; i += kThreads) k.children[i] = 0;
   for (int i = tid; i < a.hash; i += kThreads) {
@@ -387,13 +399,13 @@ template <typename U>
 __device__ __forceinline__ void update_move(const MoveArgs& m, int64_t me, int64_t warps) {
   const TableArgs& a = m.t;
   const Pools& P = m.pools;
-  if (ld(a.count) == 0) return;
+  if (gave_up(a) || ld(a.count) == 0) return;
   const int lane = threadIdx.x & 31;
   const int64_t per_seq = static_cast<int64_t>(P.n) * P.H, pages = a.n_out * per_seq;
   for (int64_t it = me; it < pages; it += warps) {
     const int s = static_cast<int>(it / per_seq);
     const int2 c = __ldcg(a.copy + s);
-    if (c.x < 0 || c.x >= a.num_pages || c.y < 0 || c.y >= a.num_pages) continue;   // (after a timeout: any)
+    if (c.x < 0) continue;
     const int rest = static_cast<int>(it - s * per_seq), t = rest / P.H, h = rest - t * P.H;
     const int rows = __ldg(a.lens + __ldg(a.parents + s)) % P.ps;
     const int64_t from = (static_cast<int64_t>(c.x) * P.H + h) * P.ps;
@@ -427,7 +439,6 @@ __device__ __forceinline__ void compact_body(const TableArgs& a) {
   __shared__ int sm[kWarps];
   Meet meet(a);
   const int n_cta = gridDim.x, cta = blockIdx.x, tid = threadIdx.x;
-  if (cta == 0 && tid == 0) a.count[0] = -1;   // nothing to move unless the plan comes to its end
   for (int b = cta; b < a.n_blk; b += n_cta) {
     const int i = b * kBlock + tid;
     const int used = __syncthreads_count(i < a.num_pages && __ldg(a.refs + i) != 0);
@@ -464,8 +475,8 @@ template <typename U>
 __device__ __forceinline__ void compact_move(const MoveArgs& m, int64_t me, int64_t warps) {
   const TableArgs& a = m.t;
   const Pools& P = m.pools;
+  if (gave_up(a)) return;
   const int moves = ld(a.count), n = ld(a.live_out);
-  if (moves < 0) return;
   const int lane = threadIdx.x & 31;
   // a page of one pool is one run of bytes: its heads' rows lie one after the other
   const int64_t codes = static_cast<int64_t>(P.H) * P.ps * P.pd, scales = static_cast<int64_t>(P.H) * P.ps;
@@ -473,7 +484,6 @@ __device__ __forceinline__ void compact_move(const MoveArgs& m, int64_t me, int6
   for (int64_t it = me; it < pages; it += warps) {
     const int i = static_cast<int>(it / P.n), t = static_cast<int>(it - static_cast<int64_t>(i) * P.n);
     const int64_t from = ld(a.from + i), to = ld(a.place + i);
-    if (from < 0 || from >= a.num_pages || to < 0 || to >= a.num_pages) continue;   // (after a timeout: any)
     warp_copy<U>(P.p[t].codes + to * codes, P.p[t].codes + from * codes, codes);
     warp_copy<uint16_t>(P.p[t].scales + to * scales, P.p[t].scales + from * scales, 2 * scales);
   }
@@ -687,7 +697,8 @@ cudaError_t launch(const MoveArgs& m, int64_t warps, int64_t bytes, cudaStream_t
 }
 
 template <bool UPDATE>
-kvq_status run(const char* fn, const MoveArgs& m, int64_t warps, int64_t bytes, kvq_stream_t stream) {
+kvq_status run(const char* fn, MoveArgs& m, int64_t warps, int64_t bytes, kvq_stream_t stream) {
+  if (plan_work<UPDATE>(m.t) <= kClusterWork) m.t.bar = nullptr;   // the plan's blocks meet without it
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   // the widest piece that divides what is copied (a row of one head, a whole page)
   const int64_t unit = UPDATE ? m.pools.pd : static_cast<int64_t>(m.pools.H) * m.pools.ps * m.pools.pd;
