@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_slice_kernel(const __grid_
   asm volatile("griddepcontrol.wait;" ::: "memory");               // started while the work before it ends
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const T* x_row = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.stride;
-  const int begin = sl * a.slice, end = min(a.vocab, begin + a.slice);
+  const int begin = sl * a.slice, end = begin + min(a.slice, a.vocab - begin);   // (begin + slice may leave int)
   const int K = a.num_out;
   const float score = __ldg(a.scores + row);
   float4* part = a.part + blockIdx.x;
