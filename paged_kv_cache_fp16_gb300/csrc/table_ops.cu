@@ -269,7 +269,7 @@ __device__ __forceinline__ void update_body(const TableArgs& a) {
   const int n_cta = gridDim.x, cta = blockIdx.x, tid = threadIdx.x;
   const int all = n_cta * kThreads, me = cta * kThreads + tid;
 
-  for (int i = me; i < a.num_pages; i += all) st(a.refs_out + i, __ldg(a.refs + i));
+  for (int64_t i = me; i < a.num_pages; i += all) st(a.refs_out + i, __ldg(a.refs + i));
   for (int i = tid; i < a.n_in; i += kThreads) k.children[i] = 0;
   for (int i = tid; i < a.hash; i += kThreads) {
     k.key[i] = -1;
@@ -420,16 +420,16 @@ __device__ __forceinline__ void update_move(const MoveArgs& m, int64_t me, int64
     const int s = static_cast<int>(it / per_row), j0 = static_cast<int>(it - static_cast<int64_t>(s) * per_row) * kRow;
     const int parent = __ldg(a.parents + s);
     if (parent < 0 || parent >= a.n_in) continue;
-    const int n = old_seq(a, parent).keep - (__ldcg(a.copy + s).x >= 0);
-    const int32_t* from = a.table + static_cast<int64_t>(parent) * a.max_pages;
-    int32_t* to = a.table_out + static_cast<int64_t>(s) * a.max_pages;
+    const int left = old_seq(a, parent).keep - (__ldcg(a.copy + s).x >= 0) - j0;   // (j0 + 256 may leave int)
+    const int32_t* from = a.table + static_cast<int64_t>(parent) * a.max_pages + j0;
+    int32_t* to = a.table_out + static_cast<int64_t>(s) * a.max_pages + j0;
     int v[kRow / 32];
 #pragma unroll
     for (int i = 0; i < kRow / 32; ++i)
-      if (j0 + 32 * i + lane < n) v[i] = __ldg(from + j0 + 32 * i + lane);
+      if (32 * i + lane < left) v[i] = __ldg(from + 32 * i + lane);
 #pragma unroll
     for (int i = 0; i < kRow / 32; ++i)
-      if (j0 + 32 * i + lane < n) to[j0 + 32 * i + lane] = v[i];
+      if (32 * i + lane < left) to[32 * i + lane] = v[i];
   }
 }
 
@@ -499,11 +499,12 @@ __device__ __forceinline__ void compact_move(const MoveArgs& m, int64_t me, int6
       if (lane == 0 && j0 == 0) report(a.err, KVQ_DEVERR_INDEX);
       held = 0;
     }
-    const int64_t row = static_cast<int64_t>(s) * a.max_pages;
+    const int64_t row = static_cast<int64_t>(s) * a.max_pages + j0;
+    const int left = held - j0;
 #pragma unroll
     for (int i = 0; i < kRow / 32; ++i) {
-      const int j = j0 + 32 * i + lane;
-      if (j >= held) continue;
+      const int j = 32 * i + lane;
+      if (j >= left) continue;
       int page = __ldg(a.table + row + j);
       if (page < 0 || page >= a.num_pages) {
         report(a.err, KVQ_DEVERR_PAGE_RANGE);
