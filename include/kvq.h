@@ -817,7 +817,8 @@ KVQ_API kvq_status kvq_table_compact(const kvq_pool* pools, int n_tensors, const
  * with shared_lens NULL is the plain decode step.
  *   out[l][s][j][:] = sum_t softmax(softmax_scale q[l][s][j] . k_t)_t v_t[:],   t in [0, seq_lens[s])
  * with k_t = code * scale, v_t likewise, not rounded (kvq_decode_attn's are, to fp16); softmax weights
- * times v's scale are rounded to fp16 for the product with v's codes, sums are float32.
+ * times v's scale are rounded to 11 bits for the product with v's codes (where one is below 2^-24 of the
+ * row's largest weight times its largest scale of V, to 2^-35 of that), sums are float32.
  * q, out     device, `dtype` (KVQ_F16 or KVQ_BF16), [n_layers][nseq][num_q_heads][D], 16-byte aligned; a
  *            sequence of length 0 gets 0.
  * k_pools, v_pools, page_table, seq_lens, dev_err  as for kvq_decode_attn; shared_lens device int32

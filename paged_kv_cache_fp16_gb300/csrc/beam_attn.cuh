@@ -23,11 +23,13 @@
 //     so that no bytes have to be brought together.  Copies of 16 bytes go to places that make it free
 //     of bank conflicts.
 //   - keys' scales multiply the scores in float32, so no product is rounded: the cache stands for
-//     code * scale exactly.  V's scales multiply the weights.
+//     code * scale exactly.  V's scales multiply the weights, and the products are rounded to fp16; the
+//     exponentials' reference keeps the largest of them between some 2^10 and 2^15, so that all but those
+//     below 2^-24 of it keep fp16's 11 bits, whatever the scales are.
 // Queries are put into fp16 with one power of two per row (that of the largest entry), so bf16 queries
 // lose nothing that a float32 sum of the row would keep.
 //
-// A block joins its warps per unit and writes one record (O, max, sum per column) to the workspace, or,
+// A block joins its warps per unit and writes one record (O, reference, sum per column) to the workspace, or,
 // where it had the whole of a row, the result; a second kernel joins the records of a sequence's prefix
 // and own tokens in a fixed order.  Record unit + place of the block in its line is nobody else's: from
 // one piece of the line to the next one of the two rises.
@@ -60,7 +62,7 @@ constexpr int kUnitCost = 8;
 // (With fewer units than blocks a block's four warps end one sooner: 4 beams of 300 tokens 14.4 against 17 us.)
 constexpr int kSoloCost = 5, kSoloUnits = 400;
 #define kNegInf (-__int_as_float(0x7f800000))
-#define kMaxFloor (-1e30f)     // floor of the running maximum; one still at it saw no token
+#define kMaxFloor (-1e30f)     // floor of the exponentials' reference; one still at it saw no token
 
 struct LayerPools {
   const uint8_t* kc;
@@ -484,11 +486,13 @@ __device__ __forceinline__ void run_piece(const BeamArgs& a, const Piece& u, flo
           }
         }
       }
-      // A new maximum is taken up when it is 2^4 above the reference or this lane's scales of V leave fp16
-      // no room for weights up to 2^4 (all 8 columns' maxima change in most of a run's first steps).
+      // The products weight * scale of V are rounded to fp16, so the reference m follows score + exponent of the
+      // scale (of this lane's largest one; 0 counts as the smallest that fp16 has): m is taken up anew, to 10 below
+      // that, when it is more than 14 below, so that products stay below 2^15 and the largest do not fall far
+      // below 2^10.  (Not at every new maximum: those of all 8 columns change in most of a run's first steps.)
       float v_most = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
       if constexpr (TP == 2) v_most = fmaxf(v_most, fmaxf(fabsf(vs[2]), fabsf(vs[3])));
-      const float slack = v_most < 4000.f ? 4.f : 0.f;
+      const float v_exp = static_cast<float>(max((__float_as_int(v_most) >> 23) - 127, -24));
       uint32_t pb[NT][2 * TP];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -507,8 +511,10 @@ __device__ __forceinline__ void run_piece(const BeamArgs& a, const Piece& u, flo
           m0 = fmaxf(m0, fmaxf(x[2][0], x[3][0]));
           m1 = fmaxf(m1, fmaxf(x[2][1], x[3][1]));
         }
-        if (__any_sync(kFullMask, m0 > m[n][0] + slack || m1 > m[n][1] + slack)) {
-          float n0 = fmaxf(m[n][0], m0), n1 = fmaxf(m[n][1], m1);
+        m0 += v_exp;
+        m1 += v_exp;
+        if (__any_sync(kFullMask, m0 > m[n][0] + 14.f || m1 > m[n][1] + 14.f)) {
+          float n0 = fmaxf(m[n][0], m0 - 10.f), n1 = fmaxf(m[n][1], m1 - 10.f);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             n0 = fmaxf(n0, __shfl_xor_sync(kFullMask, n0, o));
