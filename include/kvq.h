@@ -830,7 +830,8 @@ KVQ_API kvq_status kvq_table_compact(const kvq_pool* pools, int n_tensors, const
  *            may overlap need one each.  The size for some n_layers, nseq and bounds suffices for every call
  *            of the same beams, heads and head_dim with none of these larger.
  * head_dim 64, 128 or 256; page_size a multiple of 16; at most 64 query heads per KV head.  Two calls
- * with the same arguments give the same bits.  Queries of 2^100 and more in magnitude may give NaN.
+ * with the same arguments give the same bits.  Queries of 2^100 and more in magnitude, and scores that (times
+ * log2 e) leave float32's range, may give NaN or 0.
  * Errors: KVQ_ERR_SHAPE, KVQ_ERR_BITS (other than 4), KVQ_ERR_NULL, KVQ_ERR_ALIGN, KVQ_ERR_RANGE (nseq not
  * a multiple of beams; bounds that max_pages cannot hold; softmax_scale not in (0, 2.3e38]),
  * KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.

@@ -62,7 +62,7 @@ constexpr int kUnitCost = 8;
 // (With fewer units than blocks a block's four warps end one sooner: 4 beams of 300 tokens 14.4 against 17 us.)
 constexpr int kSoloCost = 5, kSoloUnits = 400;
 #define kNegInf (-__int_as_float(0x7f800000))
-#define kMaxFloor (-1e30f)     // floor of the exponentials' reference; one still at it saw no token
+#define kMaxFloor (-3.402823466e38f)   // floor of the exponentials' reference; one still at it saw no token
 
 struct LayerPools {
   const uint8_t* kc;
