@@ -823,8 +823,11 @@ KVQ_API kvq_status kvq_table_compact(const kvq_pool* pools, int n_tensors, const
  *            sequence of length 0 gets 0.
  * k_pools, v_pools, page_table, seq_lens, dev_err  as for kvq_decode_attn; shared_lens device int32
  *            [nseq / beams] or NULL (all 0), at most the group's lengths.
- * max_shared, max_own  host upper bounds on shared_lens and on seq_lens - shared_lens.  A group that
- *            contradicts them gets 0 (KVQ_DEVERR_INDEX).  Tokens whose page id is out of range are not
+ * max_shared, max_own  host upper bounds on shared_lens and on seq_lens - shared_lens.  Their sum must fit a
+ *            row of the table (max_pages * page_size tokens, 2^31 - 65 at most), unless max_own is all
+ *            that a row holds: for batches whose longest prefix and longest own part are of different
+ *            groups, and where nothing tighter is known.  A group whose lengths contradict the bounds or
+ *            exceed the row gets 0 (KVQ_DEVERR_INDEX).  Tokens whose page id is out of range are not
  *            attended (KVQ_DEVERR_PAGE_RANGE).
  * workspace  kvq_beam_attn_workspace(...) bytes, 16-byte aligned, no initialisation needed; two calls that
  *            may overlap need one each.  The size for some n_layers, nseq and bounds suffices for every call
@@ -833,7 +836,7 @@ KVQ_API kvq_status kvq_table_compact(const kvq_pool* pools, int n_tensors, const
  * with the same arguments give the same bits.  Queries of 2^100 and more in magnitude, and scores that (times
  * log2 e) leave float32's range, may give NaN or 0.
  * Errors: KVQ_ERR_SHAPE, KVQ_ERR_BITS (other than 4), KVQ_ERR_NULL, KVQ_ERR_ALIGN, KVQ_ERR_RANGE (nseq not
- * a multiple of beams; bounds that max_pages cannot hold; softmax_scale not in (0, 2.3e38]),
+ * a multiple of beams; bounds beyond a row of the table, see above; softmax_scale not in (0, 2.3e38]),
  * KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
  */
 KVQ_API size_t kvq_beam_attn_workspace(int n_layers, int nseq, int beams, int num_kv_heads,

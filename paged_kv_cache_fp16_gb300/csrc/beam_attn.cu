@@ -43,11 +43,13 @@ Plan plan(int n_layers, int nseq, int beams, int H, int Hq, int D, int max_share
   return p;
 }
 
+constexpr int kMostTokens = INT32_MAX - 64;   // of a sequence
+
 bool bad_shape(int n_layers, int nseq, int beams, int H, int Hq, int D, int max_shared, int max_own) {
   return n_layers < 1 || n_layers > KVQ_MAX_TENSORS || nseq < 1 || nseq > KVQ_MAX_SEQS || beams < 1 ||
          beams > KVQ_MAX_BEAMS || nseq % beams != 0 || H < 1 || Hq < 1 || Hq % H != 0 ||
          Hq / H > 64 || (D != 64 && D != 128 && D != 256) || max_shared < 0 || max_own < 0 ||
-         static_cast<int64_t>(max_shared) + max_own > INT32_MAX - 64;
+         max_shared > kMostTokens || max_own > kMostTokens;
 }
 
 }  // namespace
@@ -97,11 +99,14 @@ extern "C" kvq_status kvq_beam_attn(kvq_dtype dtype, const kvq_pool* k_pools, co
   if (nseq < 0 || nseq > KVQ_MAX_SEQS || nseq % beams != 0)
     return fail(KVQ_ERR_RANGE, "%s: nseq %d must be a multiple of beams, at most %d", fn, nseq,
                 KVQ_MAX_SEQS);
-  if (max_pages < 1 || max_shared < 0 || max_own < 0 ||
-      static_cast<int64_t>(max_shared) + max_own > INT32_MAX - 64 ||
-      static_cast<int64_t>(max_shared) + max_own > static_cast<int64_t>(max_pages) * p0.page_size)
-    return fail(KVQ_ERR_RANGE, "%s: max_shared %d, max_own %d, max_pages %d", fn, max_shared, max_own,
-                max_pages);
+  // The longest prefix and the longest own part may be of different groups; that a row of the table holds their
+  // sum is asked for all the same, as a check of the bounds, unless max_own is all that it holds.
+  const int max_len =
+      static_cast<int>(std::min<int64_t>(static_cast<int64_t>(max_pages) * p0.page_size, kMostTokens));
+  if (max_pages < 1 || max_shared < 0 || max_own < 0 || max_shared > max_len || max_own > max_len ||
+      (static_cast<int64_t>(max_shared) + max_own > max_len && max_own != max_len))
+    return fail(KVQ_ERR_RANGE, "%s: max_shared %d, max_own %d where a row of the table holds %d tokens", fn,
+                max_shared, max_own, max_len);
   if (!shared_lens && max_shared != 0)
     return fail(KVQ_ERR_NULL, "%s: max_shared without shared_lens", fn);
   if (!(softmax_scale > 0.f && softmax_scale <= 2.3e38f))
@@ -132,7 +137,7 @@ extern "C" kvq_status kvq_beam_attn(kvq_dtype dtype, const kvq_pool* k_pools, co
   a.H = H; a.G = num_q_heads / H; a.Hq = num_q_heads; a.ps = p0.page_size;
   a.max_pages = max_pages; a.n_layers = n_layers;
   a.line[0] = p.line[0]; a.line[1] = p.line[1];
-  a.max_shared = max_shared; a.max_own = max_own;
+  a.max_shared = max_shared; a.max_own = max_own; a.max_len = max_len;
   a.magic = 0x64006400u;
   a.scale = softmax_scale * 1.4426950408889634f;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

@@ -90,7 +90,7 @@ struct BeamArgs {
   int32_t* err;
   int nseq, beams, groups, H, G, Hq, ps, max_pages, n_layers;
   Line line[2];                        // prefixes, own tokens
-  int max_shared, max_own;
+  int max_shared, max_own, max_len;    // max_len: what a row of the table holds
   uint32_t magic;
   float scale;                         // softmax_scale * log2(e)
 };
@@ -151,7 +151,7 @@ __device__ __forceinline__ bool group_ok(const BeamArgs& a, int g, int& sh) {
 #pragma unroll 4
   for (int i = 0; i < a.beams; ++i) {
     const int len = __ldg(a.lens + g * a.beams + i);
-    ok = ok && len >= sh && len - sh <= a.max_own;
+    ok = ok && len >= sh && len - sh <= a.max_own && len <= a.max_len;
   }
   return ok && sh >= 0 && sh <= a.max_shared;
 }
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, (kResident<D, NT>)) beam_attn_kernel
 #pragma unroll 4
     for (int i = 0; i < a.beams; ++i) {
       const int len = __ldg(a.lens + g * a.beams + i);
-      ok = ok && len >= sh && len - sh <= a.max_own;
+      ok = ok && len >= sh && len - sh <= a.max_own && len <= a.max_len;
       own += unit_cost(span_from(sh, len, ok).granules, a.line[1]);
     }
     if (ok) {
