@@ -719,7 +719,8 @@ KVQ_API kvq_status kvq_tree_commit(const kvq_pool* pools, int n_tensors, const i
 /*
  * The step that decides which beams go on.  With x[b][v] the logits behind beam b of a sequence and
  *   t[b][v] = scores[b] + x[b][v] - log sum_w exp x[b][w]
- * the num_out candidates of largest t, in falling order, equal ones by beam and then token:
+ * the num_out candidates of largest t, in falling order, equal ones by beam and then token (those of one
+ * beam that only float64 makes equal, behind a far score or near logits, by logit first):
  *   out_scores  float32 [nseq][num_out]   t
  *   out_parents int32 [nseq][num_out]     the candidate's row s * beams + b
  *   out_tokens  int32 [nseq][num_out]     v

@@ -603,20 +603,18 @@ __device__ __forceinline__ double log64(double x) {
   return y + (x * exp64(-y) - 1.);
 }
 
+// A candidate; its beam stands beside it.  Equal scores of one beam go by the logit first: different logits have
+// equal t in float64 behind a far score, and where they are much nearer to each other than to the sum.
 struct Cand {
   uint64_t score;   // ordered(double)
-  uint32_t at;      // beam
-  uint32_t token;
-  __device__ __forceinline__ bool above(const Cand& o) const {
-    if (score != o.score) return score > o.score;
-    return at != o.at ? at < o.at : token < o.token;
-  }
+  uint64_t key;     // logit, then token: the larger one first
 };
 
 __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_constant__ SelectArgs a) {
   __shared__ double lse[KVQ_MAX_BEAMS], pair[KVQ_MAX_BEAMS][kPairs];
   __shared__ float most[KVQ_MAX_BEAMS];
   __shared__ Cand list[kRound + kKeep], other[kKeep];
+  __shared__ uint8_t list_beam[kRound + kKeep], other_beam[kKeep];
   __shared__ int n_list;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = blockIdx.x, K = a.num_out;
@@ -684,7 +682,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
       const double x = static_cast<double>(unordered(static_cast<uint32_t>(raw[j].key >> 32)));
       const double t = (x - lse[raw[j].beam]) + raw[j].score;
       if (!(t > static_cast<double>(kNegInf))) continue;   // NaN and -inf
-      mine[j] = Cand{ordered(t), static_cast<uint32_t>(raw[j].beam), ~static_cast<uint32_t>(raw[j].key)};
+      mine[j] = Cand{ordered(t), raw[j].key};
     }
     if (c0 == 0 && all > 128) {
       // the num_out-th largest of the threads' best, by the upper half of the order (beams are so
@@ -702,19 +700,34 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
     }
 #pragma unroll
     for (int j = 0; j < kRound / kThreads; ++j)
-      if (mine[j].score && mine[j].score >= low) list[atomicAdd(&n_list, 1)] = mine[j];
+      if (mine[j].score && mine[j].score >= low) {
+        const int to = atomicAdd(&n_list, 1);
+        list[to] = mine[j];
+        list_beam[to] = static_cast<uint8_t>(raw[j].beam);
+      }
     __syncthreads();
     n = n_list;
     for (int i = warp; i < n; i += kWarps) {
       const Cand x = list[i];
+      const int beam = list_beam[i];
       int r = 0;
-      for (int j = lane; j < n; j += 32) r += list[j].above(x);
+      for (int j = lane; j < n; j += 32) {
+        const Cand o = list[j];
+        r += o.score != x.score ? o.score > x.score
+             : list_beam[j] != beam ? list_beam[j] < beam : o.key > x.key;
+      }
       r = __reduce_add_sync(kFullMask, r);
-      if (r < K && lane == 0) other[r] = x;
+      if (r < K && lane == 0) {
+        other[r] = x;
+        other_beam[r] = static_cast<uint8_t>(beam);
+      }
     }
     n = min(n, K);
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) list[i] = other[i];
+    for (int i = tid; i < n; i += kThreads) {
+      list[i] = other[i];
+      list_beam[i] = other_beam[i];
+    }
     if (tid == 0) n_list = n;
     if (n == K) low = other[K - 1].score;
     __syncthreads();
@@ -727,8 +740,8 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
       const uint64_t u = list[i].score;
       score = static_cast<float>(__longlong_as_double(static_cast<long long>(
           u & 0x8000000000000000ull ? u ^ 0x8000000000000000ull : ~u)));
-      parent = static_cast<int>(row0) + static_cast<int>(list[i].at);
-      token = static_cast<int>(list[i].token);
+      parent = static_cast<int>(row0) + list_beam[i];
+      token = static_cast<int>(~static_cast<uint32_t>(list[i].key));
     }
     a.out_scores[o] = score;
     a.out_parents[o] = parent;
