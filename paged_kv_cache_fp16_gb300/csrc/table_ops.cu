@@ -53,12 +53,13 @@ struct TableArgs {
   const int32_t *table, *lens, *held, *refs, *parents, *room;
   int32_t *table_out, *lens_out, *held_out, *refs_out, *live_out;
   int32_t* err;
-  int32_t* bar;                        // a grid's plan: arrivals, blocks that gave up waiting; NULL for other plans
+  int32_t* bar;                        // a grid's plan: arrivals
   int32_t* blk;                        // free (update) or used (compact) pages per block
   int32_t *place, *from;               // compact: place of rank i, page of rank i
   int32_t* rank;                       // compact: per page
   int2* copy;                          // update, per new sequence: its copied page and where to, or -1
-  int32_t* count;                      // [0]: moves (compact); new sequences whose rows are written (update)
+  int2* count;                         // x: moves (compact); new sequences whose rows are written (update)
+                                       // y: blocks that gave up waiting
   int ps, max_pages, n_in, n_out, num_pages, n_blk, hash;   // hash: slots, a power of two
 };
 
@@ -70,6 +71,7 @@ struct MoveArgs {
 // ------------------------------------------------------------------- how the blocks of a call meet
 // One block.
 struct BlockMeet {
+  static constexpr bool kSure = true;
   __device__ explicit BlockMeet(const TableArgs&) {}
   __device__ bool operator()() {
     __threadfence_block();
@@ -80,6 +82,7 @@ struct BlockMeet {
 
 // One cluster: the hardware's barrier.
 struct ClusterMeet {
+  static constexpr bool kSure = true;
   __device__ explicit ClusterMeet(const TableArgs&) {}
   __device__ bool operator()() {
     __syncthreads();
@@ -94,14 +97,14 @@ struct ClusterMeet {
 #define KVQ_MEET_WAIT_LIMIT (1LL << 22)
 #endif
 
-// A cooperative grid: arrivals counted in global memory (zeroed before the launch), with a bounded
-// wait.  A block that gave up leaves the others to their own limits, reports it and is counted: the blocks
-// that met after all do not know of it, so the moves ask whether there was one.
+// A cooperative grid: arrivals counted in global memory (zeroed before the launch, as `count` is), with a
+// bounded wait.  A block that gave up leaves the others to their own limits, reports it and is counted: the
+// blocks that met after all do not know of it, so the moves look whether there was one.
 struct GridMeet {
-  int32_t* bar;
-  int32_t* err;
+  static constexpr bool kSure = false;
+  int32_t *bar, *gone, *err;
   int goal = 0;
-  __device__ explicit GridMeet(const TableArgs& a) : bar(a.bar), err(a.err) {}
+  __device__ explicit GridMeet(const TableArgs& a) : bar(a.bar), gone(&a.count->y), err(a.err) {}
   __device__ bool operator()() {
     goal += gridDim.x;
     __threadfence();
@@ -116,7 +119,7 @@ struct GridMeet {
         met = v >= goal;
       }
       if (!met) {
-        atomicAdd(bar + 1, 1);
+        atomicAdd(gone, 1);
         report(err, KVQ_DEVERR_TIMEOUT);
       }
       __threadfence();
@@ -129,8 +132,13 @@ struct GridMeet {
 __device__ __forceinline__ int ld(const int32_t* p) { return __ldcg(p); }
 __device__ __forceinline__ void st(int32_t* p, int v) { __stcg(p, v); }
 
-// Whether a block of the plan gave up: then what it had to write holds anything, and nothing is moved.
-__device__ __forceinline__ bool gave_up(const TableArgs& a) { return a.bar && ld(a.bar + 1) != 0; }
+// What the plan leaves to the moves.  Where a block gave up, what it had to write holds anything, and nothing
+// is moved.
+template <typename Meet>
+__device__ __forceinline__ void put_count(const TableArgs& a, int n) {
+  if constexpr (Meet::kSure) *a.count = make_int2(n, 0);
+  else a.count->x = n;
+}
 
 // Sum over the block; every thread gets it.
 __device__ __forceinline__ int block_sum(int v, int* sm) {
@@ -269,7 +277,8 @@ __device__ __forceinline__ void update_body(const TableArgs& a) {
   const int n_cta = gridDim.x, cta = blockIdx.x, tid = threadIdx.x;
   const int all = n_cta * kThreads, me = cta * kThreads + tid;
 
-  for (int64_t i = me; i < a.num_pages; i += all) st(a.refs_out + i, __ldg(a.refs + i));
+  for (uint32_t i = me; i < static_cast<uint32_t>(a.num_pages); i += all)   // (the last step may leave int)
+    st(a.refs_out + i, __ldg(a.refs + i));
   for (int i = tid; i < a.n_in; i += kThreads) k.children[i] = 0;
   for (int i = tid; i < a.hash; i += kThreads) {
     k.key[i] = -1;
@@ -367,7 +376,7 @@ __device__ __forceinline__ void update_body(const TableArgs& a) {
   const bool enough = total <= sum_of(a.blk, a.n_blk, sm);   // the same in every block
   if (me == 0) {
     if (!enough) report(a.err, KVQ_DEVERR_NO_PAGES);
-    a.count[0] = enough ? a.n_out : 0;
+    put_count<Meet>(a, enough ? a.n_out : 0);
   }
   if (!enough) return;
   for (int b = cta; b < a.n_blk; b += n_cta) {
@@ -399,7 +408,8 @@ template <typename U>
 __device__ __forceinline__ void update_move(const MoveArgs& m, int64_t me, int64_t warps) {
   const TableArgs& a = m.t;
   const Pools& P = m.pools;
-  if (gave_up(a) || ld(a.count) == 0) return;
+  const int2 count = __ldcg(a.count);
+  if (count.x == 0 || count.y != 0) return;
   const int lane = threadIdx.x & 31;
   const int64_t per_seq = static_cast<int64_t>(P.n) * P.H, pages = a.n_out * per_seq;
   for (int64_t it = me; it < pages; it += warps) {
@@ -467,7 +477,7 @@ __device__ __forceinline__ void compact_body(const TableArgs& a) {
   }
   if (cta == 0 && tid == 0) {
     *a.live_out = n;
-    a.count[0] = n - stay;
+    put_count<Meet>(a, n - stay);
   }
 }
 
@@ -475,8 +485,9 @@ template <typename U>
 __device__ __forceinline__ void compact_move(const MoveArgs& m, int64_t me, int64_t warps) {
   const TableArgs& a = m.t;
   const Pools& P = m.pools;
-  if (gave_up(a)) return;
-  const int moves = ld(a.count), n = ld(a.live_out);
+  const int2 count = __ldcg(a.count);
+  const int moves = count.x, n = ld(a.live_out);
+  if (count.y != 0) return;
   const int lane = threadIdx.x & 31;
   // a page of one pool is one run of bytes: its heads' rows lie one after the other
   const int64_t codes = static_cast<int64_t>(P.H) * P.ps * P.pd, scales = static_cast<int64_t>(P.H) * P.ps;
@@ -575,7 +586,7 @@ Plan plan(int64_t num_pages, int64_t nseq) {
     return here;
   };
   p.bar = take(4);
-  p.count = take(4);
+  p.count = take(4);       // (behind bar: they are zeroed together)
   p.place = take(num_pages);
   p.from = take(num_pages);
   p.rank = take(num_pages);
@@ -634,7 +645,7 @@ kvq_status common(const char* fn, MoveArgs& m, const kvq_pool* pools, int n_tens
   const Plan p = plan(a.num_pages, std::max(n_in, n_out));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   auto at = [&](size_t o) { return reinterpret_cast<int32_t*>(ws + o); };
-  a.bar = at(p.bar); a.count = at(p.count); a.place = at(p.place); a.from = at(p.from);
+  a.bar = at(p.bar); a.count = reinterpret_cast<int2*>(ws + p.count); a.place = at(p.place); a.from = at(p.from);
   a.rank = at(p.rank); a.blk = at(p.blk);
   a.copy = reinterpret_cast<int2*>(ws + p.copy);
   a.hash = 64;
@@ -671,7 +682,7 @@ cudaError_t launch_plan(const TableArgs& a, cudaStream_t cs) {
   }
   e = grid.allow(plan_grid_kernel<UPDATE>, kMostSmem);
   if (e != cudaSuccess) return e;
-  e = cudaMemsetAsync(a.bar, 0, 16, cs);
+  e = cudaMemsetAsync(a.bar, 0, 32, cs);   // bar and count
   if (e != cudaSuccess) return e;
   TableArgs copy = a;
   void* args[] = {&copy};
@@ -698,8 +709,7 @@ cudaError_t launch(const MoveArgs& m, int64_t warps, int64_t bytes, cudaStream_t
 }
 
 template <bool UPDATE>
-kvq_status run(const char* fn, MoveArgs& m, int64_t warps, int64_t bytes, kvq_stream_t stream) {
-  if (plan_work<UPDATE>(m.t) <= kClusterWork) m.t.bar = nullptr;   // the plan's blocks meet without it
+kvq_status run(const char* fn, const MoveArgs& m, int64_t warps, int64_t bytes, kvq_stream_t stream) {
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   // the widest piece that divides what is copied (a row of one head, a whole page)
   const int64_t unit = UPDATE ? m.pools.pd : static_cast<int64_t>(m.pools.H) * m.pools.ps * m.pools.pd;
