@@ -244,17 +244,19 @@ class Pool:
         self.__dict__.pop("_head", None)
 
     def head(self) -> tuple[int, int, int]:
-        """The four sizes as the first two 64-bit words of a kvq_pool, and the bytes of a page's codes:
+        """The four sizes as the first two 64-bit words of a kvq_pool, and the elements of a page's codes:
         formed once for their values."""
-        row = max(kvq_packed_dim(self.head_dim, self.bits), 1)      # unsupported sizes: the library refuses
-        h = (self.bits | self.num_heads << 32, self.head_dim | self.page_size << 32,
-             max(self.num_heads * self.page_size * row, 1))
-        self.__dict__["_head"] = h
+        c = self.codes
+        h = self.__dict__["_head"] = (*_sizes(self), max(c.numel() // max(c.shape[0], 1), 1))
         return h
 
     def as_c(self) -> kvq_pool:
         return kvq_pool(self.bits, self.num_heads, self.head_dim, self.page_size,
                         self.num_pages, self.codes.data_ptr(), self.scales.data_ptr())
+
+
+def _sizes(p) -> tuple[int, int]:
+    return p.bits | p.num_heads << 32, p.head_dim | p.page_size << 32
 
 
 def _pool_array(pools: Sequence[Pool]):
@@ -830,12 +832,17 @@ def _pool_words(pools: Sequence[Pool], dev: int) -> array.array:
     field."""
     words = []
     for p in pools:
-        d = p.__dict__
-        c, s = d["codes"], d["scales"]
+        if type(p) is Pool:             # its sizes are kept until they are set anew
+            d = p.__dict__
+            c, s = d["codes"], d["scales"]
+            a, b, page = d.get("_head") or p.head()
+            pages = c.numel() // page
+        else:                           # any class with a pool's attributes will do
+            c, s = p.codes, p.scales
+            (a, b), pages = _sizes(p), c.shape[0]
         if c.get_device() != dev or s.get_device() != dev:
             raise ValueError("the pools are not on the current device")
-        a, b, page = d.get("_head") or p.head()
-        words += (a, b, c.numel() // page, c.data_ptr(), s.data_ptr())
+        words += (a, b, pages, c.data_ptr(), s.data_ptr())
     return array.array("Q", words)
 
 
