@@ -89,3 +89,13 @@ def tolerance(n, o, size, score, top, v_most, kind):
     least = 2.0 ** -25 if kind == "f16" else 0.0
     return (size * (2.0 ** -11 + 2 * e[:, None] + 2.0 ** -17) + 1.001 * STEP[kind] * np.abs(o) + least
             + (8 * n * 2.0 ** -35 * v_most * top)[:, None])
+
+
+def tiles(D, n, seed):
+    """A group whose tiles of 16 tokens can be told apart: a tile's values are 7 in one channel (tiles take the
+    channels in turn), and its score is one of 16 levels that the channel has, over a range of some 5."""
+    t = np.arange(n) // 16 % D
+    level = np.random.default_rng(seed).permutation(D) % 16
+    vc = np.zeros((n, D), np.int64)
+    vc[np.arange(n), t] = 7
+    return np.ones((n, D), np.int64), level[t] / 3 + 0.25, vc, np.full(n, 0.25)
