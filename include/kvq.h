@@ -729,8 +729,10 @@ KVQ_API kvq_status kvq_tree_commit(const kvq_pool* pools, int n_tensors, const i
  * rest is -inf, -1, -1.  With num_out = beams, out_parents is what kvq_table_update takes; a caller
  * that ends beams at a token asks for more and drops some.  A first step has one beam of score 0, the
  * others -inf (their logits are not read).
- * The order is that of t to 1e-7 at least (sums of exponentials are kept beyond float32); within a
- * beam it is exactly that of the logits.  Two calls with the same arguments give the same bits.
+ * Within a beam the order is exactly that of the logits; between beams it is that of t up to what the rows'
+ * log-sums are off: 2e-7 in the worst rows tried, 6e-8 in ordinary ones, below 2^-16 for any logits of up to
+ * 2^17 tokens (the exponentials are float32's: 2^-22, and 2^-23 of their argument).  Two calls with the same
+ * arguments give the same bits.
  * logits     device, `dtype` (KVQ_F16, KVQ_BF16 or KVQ_F32), nseq * beams rows of vocab elements,
  *            row_stride >= vocab elements apart; any alignment.
  * scores     device float32 [nseq][beams].
