@@ -9,8 +9,9 @@
 // equal cost, so lengths of any kind load the GPU evenly; every block finds its share from the lengths by
 // itself.  Where a unit has more columns than a block, neighbouring blocks take the same tokens at the same
 // time.  A block's four warps take a granule's steps of 32 tokens, each with a ring of asynchronous copies
-// of its own.  Where no sequence has more own tokens than a granule, a unit of them is one warp's: it costs
-// more to start and end than to attend (63 groups of 8 beams with up to 107 own tokens: 89 to 63 us).  Tokens are the products' M:
+// of its own.  Where the call's bound says that no sequence has more own tokens than a granule, a unit of them
+// is one warp's: it costs more to start and end than to attend (63 groups of 8 beams with up to 107 own
+// tokens: 89 to 63 us).  Tokens are the products' M:
 //   S^T[16 x 8 NT] = K[16 x D] Q^T,  online softmax per column,  O^T[D x 8 NT] += V^T[D x 16] P^T
 // What bounds it is the unpacking of the codes, so that is spent once per NT column tiles, and little:
 //   - a 4-bit code u = c + 8 in bits 0-3 of a 16-bit lane, with fp16's 1024 set above it, is 1024 + u,
@@ -56,7 +57,8 @@ constexpr int kTile = 16;
 constexpr int kStep = 2 * kTile;             // tokens of a warp's step
 constexpr int kGranule = kWarps * kStep;     // tokens of a block's step
 constexpr int kMostBlocks = 152 * 3;
-// Cost of starting and ending a unit in a block; a granule's is 2 (unpacking) and 1 per column tile.
+// Cost of starting and ending a unit in a block; a granule's is 2 (unpacking) and 1 per column tile.  (Fitted
+// at 128 channels: 5 gave equal times, 12 gave 47 instead of 45 us for 64 sequences.)
 constexpr int kUnitCost = 8;
 // Where own tokens are one granule at most, a unit is a warp's, four of a sequence a block's at once.
 // (With fewer units than blocks a block's four warps end one sooner: 4 beams of 300 tokens 14.4 against 17 us.)
@@ -236,7 +238,8 @@ __device__ __forceinline__ float pow2_rest(int e) { return __int_as_float((e - e
 
 // Blocks per SM: fewer than the registers allow.  Every block more makes the shares shorter, of which each
 // costs its start and end (7 + 2 us): 64 sequences of up to 8,192 tokens of 128 channels 44.8 us with 4,
-// 41.8 with 3, 42.5 with 2; up to 32,768 tokens 123, 114 and 120.
+// 41.8 with 3, 42.5 with 2; up to 32,768 tokens 123, 114 and 120.  (Measured at one column tile; 64 channels
+// with one and two take the same three.)
 template <int D, int NT> constexpr int kResident = NT * D >= 256 ? 2 : 3;
 
 // d = a b + c and d += a b, free to be scheduled among each other.

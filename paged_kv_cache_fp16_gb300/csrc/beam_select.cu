@@ -11,15 +11,16 @@
 // maxima that at least num_out elements reach; the num_out-th largest element of it is the bound for the
 // later ones, so that an element costs little but its exponential and the warps need not meet.  (One warp
 // finding that bound while the others go on with the old one: 36 instead of 29 us, the old one lets too many
-// by.)  Where too many pass (logits that rise along the vocabulary), the slice is gone through again, meeting after every
-// vector to raise the bound.  Two batches are on their way (asynchronous copies, a ring per warp) while one
-// is worked on: with one, loaded to registers, the kernel waited for memory most of the time (26 us).
+// by.)  Where too many pass (logits that rise along the vocabulary), the slice is gone through again, meeting
+// after every vector to raise the bound.  Two batches are on their way (asynchronous copies, a ring per warp)
+// while one is worked on: with one, loaded to registers, the kernel waited for memory most of the time (26 us).
 //
 // Candidates of different beams are close, so the sums add little to what the exponentials are off (2^-22, and
 // two roundings of their argument): the argument is multiplied by log2 e in two parts, the terms of a thread's
 // batch are added in float32 and then to a pair of floats, and slices are joined in float64.  Against 64 bits a
-// row's log-sum is 6e-8 off in ordinary rows, 2e-7 where all terms lie at one distance.  Where elements lie in the block's threads does not depend
-// on the row's address, so that equal rows have equal sums (and ties between them stay ties).
+// row's log-sum is 6e-8 off in ordinary rows, 2e-7 where all terms lie at one distance.  Where elements lie in
+// the block's threads does not depend on the row's address, so that equal rows have equal sums (and ties
+// between them stay ties).
 #include <cstdint>
 #include <algorithm>
 #include <initializer_list>
@@ -752,7 +753,8 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const __grid_cons
 
 // Slices per row, of `spread` elements times a whole number.  A block costs about as much as 3 microseconds
 // of its stream for its start, the first bound and the end; a spread of every thread's 16 bytes takes 0.37
-// where two blocks share an SM.  The fewest microseconds over the rounds of 304 blocks win.
+// where two blocks share an SM (both fitted to bf16 rows; float32's bytes go at the same rate, but half as
+// many elements).  The fewest microseconds over the rounds of 304 blocks (two on each of 152 SMs) win.
 // Rows are cut into kMostCut slices in all at most, so that a workspace serves every smaller call.
 constexpr int64_t kMostCut = 2 * 304;
 

@@ -3,11 +3,11 @@
 //
 // The count of a page's owners is the only state: a page is free where it is 0.  Both operators read
 // tables and counts and write new ones, so that nothing has to be undone and a call can be repeated.
-// Each is two launches (one, where there is little of both): a plan, whose blocks meet between its phases, and the moves of pages and rows of
-// the tables by the whole GPU, started early.  What bounds them: the phases' meetings and chains of
-// dependent reads where little is to be moved (4 beams, one layer: 9.4 us in a graph; 64 beams over 262,000
-// tokens: 21 us of plan that reads 2.9 MB), the copied pages' bytes where much is (32 pools, 3,200 pages of
-// each: 49 us of moves at 6.3 TB/s).
+// Each is two launches (one, where there is little of both): a plan, whose blocks meet between its phases,
+// and the moves of pages and rows of the tables by the whole GPU, started early.  What bounds them: the
+// phases' meetings and chains of dependent reads where little is to be moved (4 beams, one layer: 8.5 us in a
+// graph; 64 beams over 262,000 tokens: 24.6 us, 21 of them the plan that reads 2.9 MB), the copied pages'
+// bytes where much is (32 pools, 3,200 pages of each: 53 us, 49 of them moves at 6.3 TB/s).
 //
 //   update:  counts copied; every block learns all sequences, counts children and finds page writers in
 //            its shared memory | every table entry changes its page's count by (children - 1) | pages
