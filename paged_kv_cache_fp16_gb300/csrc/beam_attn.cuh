@@ -493,9 +493,12 @@ __device__ __forceinline__ void run_piece(const BeamArgs& a, const Piece& u, flo
       // scale (of this lane's largest one; 0 counts as the smallest that fp16 has): m is taken up anew, to 10 below
       // that, when it is more than 14 below, so that products stay below 2^15 and the largest do not fall far
       // below 2^10.  (Not at every new maximum: those of all 8 columns change in most of a run's first steps.)
+      // Scores whose neighbours are further apart than that: the differences taken here are exact, and m is
+      // rounded up, but never above the score, so that the largest weight is 1 or more.
       float v_most = fmaxf(fabsf(vs[0]), fabsf(vs[1]));
       if constexpr (TP == 2) v_most = fmaxf(v_most, fmaxf(fabsf(vs[2]), fabsf(vs[3])));
       const float v_exp = static_cast<float>(max((__float_as_int(v_most) >> 23) - 127, -24));
+      const float v_below = fminf(v_exp, 10.f) - 10.f;
       uint32_t pb[NT][2 * TP];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -514,10 +517,8 @@ __device__ __forceinline__ void run_piece(const BeamArgs& a, const Piece& u, flo
           m0 = fmaxf(m0, fmaxf(x[2][0], x[3][0]));
           m1 = fmaxf(m1, fmaxf(x[2][1], x[3][1]));
         }
-        m0 += v_exp;
-        m1 += v_exp;
-        if (__any_sync(kFullMask, m0 > m[n][0] + 14.f || m1 > m[n][1] + 14.f)) {
-          float n0 = fmaxf(m[n][0], m0 - 10.f), n1 = fmaxf(m[n][1], m1 - 10.f);
+        if (__any_sync(kFullMask, m0 - m[n][0] + v_exp > 14.f || m1 - m[n][1] + v_exp > 14.f)) {
+          float n0 = fmaxf(m[n][0], __fadd_ru(m0, v_below)), n1 = fmaxf(m[n][1], __fadd_ru(m1, v_below));
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             n0 = fmaxf(n0, __shfl_xor_sync(kFullMask, n0, o));
